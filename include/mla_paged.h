@@ -32,12 +32,12 @@
  *   - With MLA_PAGED_LOG set in the environment (to anything but "0"; read once
  *     per process) every kernel launch prints one line to stderr naming the
  *     kernel, its grid and block sizes and its shapes.
- *   - Index contents in device memory (offsets, page ids) are the caller's
+ *   - Index contents in device memory (offsets, positions, page ids) are the caller's
  *     contract and are not validated on the host.  Read paths clamp every page
  *     id, page index and row to the buffers they were given, so a bad index
  *     yields unspecified values in the output rows it affects but never an
  *     access outside the pool, the weight or the outputs.  Write paths
- *     (kv_matmul_paged, mla_write_latent_paged(_fp8)) store nothing for a token
+ *     (kv_matmul_paged, mla_write_latent_paged(_fp8)(_at)) store nothing for a token
  *     whose position lies past its request's page table or whose page id lies
  *     past the pool; every other byte of the pool keeps its value.
  *   - Shapes whose 256-row tiles would need byte offsets of 2^31 or more (a
@@ -545,6 +545,268 @@ mla_status_t kv_matmul_paged(const void* hidden_state, const uint32_t* input_row
  */
 mla_status_t mla_check_indices(const uint32_t* row_offsets, const uint32_t* cache_offsets,
                                int32_t rows, const mla_paged_cache_t* cache, int64_t* bad_request,
+                               void* stream);
+
+/*
+ * Rotary positions.  A freqs_cis table row p holds, for rope pair j, (cos, sin) of the
+ * pair's angle at position p in columns 2j and 2j+1, whatever the layout of the columns
+ * that are rotated:
+ *   MLA_ROPE_INTERLEAVED  pair j is columns (2j, 2j+1) of the rope part
+ *   MLA_ROPE_HALF         pair j is columns (j, j + d_rope/2)
+ *   (x0, x1) -> (x0*c - x1*s, x0*s + x1*c)
+ */
+typedef enum {
+    MLA_ROPE_INTERLEAVED = 0,
+    MLA_ROPE_HALF = 1
+} mla_rope_layout_t;
+
+/* How a table's frequencies f_j = theta^(-2j/d_rope) are scaled for contexts longer
+ * than the original ones. */
+typedef enum {
+    MLA_ROPE_SCALING_NONE = 0,
+    MLA_ROPE_SCALING_LINEAR = 1,     /* f_j / factor: positions interpolated */
+    MLA_ROPE_SCALING_BY_PARTS = 2    /* f_j / factor where a pair turns fewer than beta_slow
+                                        times in original_max_position positions, f_j where
+                                        more than beta_fast times, mixed linearly in j between */
+} mla_rope_scaling_t;
+
+typedef struct {
+    double theta;                    /* > 0, and > 1 with BY_PARTS */
+    double factor;                   /* > 0 (LINEAR, BY_PARTS) */
+    double beta_fast;                /* BY_PARTS: > 0 */
+    double beta_slow;                /* BY_PARTS: > 0 */
+    double amplitude;                /* every cos and sin is multiplied by it */
+    int32_t scaling;                 /* mla_rope_scaling_t */
+    int32_t original_max_position;   /* BY_PARTS: > 0 */
+} mla_rope_params_t;
+
+/*
+ * Fill rows of a freqs_cis table (the freqs_cis argument of the latent write and of
+ * mla_rope_q; page "mla_prefill_decode_graph_fp8", Args freqs_cis):
+ *
+ *   freqs_cis[i][2j]   = float(amplitude * cos((first_position + i) * g_j))
+ *   freqs_cis[i][2j+1] = float(amplitude * sin((first_position + i) * g_j))
+ *   g_j = f_j                                          (NONE),  f_j = theta^(-2j/d_rope)
+ *   g_j = f_j / factor                                 (LINEAR)
+ *   g_j = f_j / factor * r_j + f_j * (1 - r_j)         (BY_PARTS)
+ *     r_j  = clamp((j - low) / max(high - low, 0.001), 0, 1)
+ *     low  = max(floor(pair(beta_fast)), 0),  high = min(ceil(pair(beta_slow)), d_rope - 1)
+ *     pair(b) = d_rope * ln(original_max_position / (2 pi b)) / (2 ln theta)
+ *   (the by-parts interpolation published as YaRN, Peng et al. 2023).
+ *
+ * The frequencies and each angle's reduction to a quarter turn are in binary64, the
+ * sine and cosine of the reduced angle in binary32.
+ *
+ * params          [host]
+ * first_position  >= 0; first_position + rows <= 2^31
+ * d_rope          even, 2 <= d_rope <= 512
+ * freqs_cis       [device] float [rows][d_rope], 8-byte aligned, written
+ * Parameters that are not finite or out of the ranges above: MLA_ERR_INVALID_SHAPE.
+ */
+mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t first_position, int32_t rows,
+                            int32_t d_rope, float* freqs_cis, void* stream);
+
+/*
+ * Rotate the rope part of every query head at its token's position (page
+ * "mla_prefill_decode_graph_fp8", Args q [tot_seq_len, num_heads, qk_nope_head_dim +
+ * qk_rope_head_dim], freqs_cis): the step before mla_absorb_q, which carries the rope
+ * columns over as they are.
+ *
+ *   q_out[t][h][0:d_nope]  = q[t][h][0:d_nope]
+ *   q_out[t][h][d_nope:]   = q[t][h][d_nope:] rotated with freqs_cis[positions[t]]
+ *   binary32 arithmetic, rounded to `dtype` (round to nearest even).
+ *
+ * positions are given, not derived from the cache: a drafted token's position is its
+ * depth in the tree, not the slot its row is stored in.  A position past the table takes
+ * the table's last row.
+ *
+ * q, q_out        [device] rows of d_nope + d_rope contiguous elements at
+ *                 t * stride_token + h * stride_head (elements, one pair of strides each),
+ *                 16-byte aligned, strides and d_nope multiples of 16 bytes.  q_out == q
+ *                 with the same strides rotates in place and touches the rope columns only;
+ *                 any other overlap is not allowed.
+ * total_tokens    [host] T >= 0;  num_heads >= 1;  T * num_heads * (d_nope + d_rope) < 2^40
+ * d_nope          0 <= d_nope <= 4096
+ * d_rope          8 <= d_rope <= 512; % 8 == 0, and % 16 == 0 with MLA_ROPE_HALF
+ * dtype           MLA_DTYPE_BF16 or MLA_DTYPE_F32
+ * positions       [device] uint32 [total_tokens]
+ * freqs_cis       [device] float [max_seq_len][d_rope], 16-byte aligned
+ */
+mla_status_t mla_rope_q(const void* q, int64_t q_stride_token, int64_t q_stride_head, int32_t total_tokens,
+                        int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t dtype,
+                        const uint32_t* positions, const float* freqs_cis, int32_t max_seq_len, int32_t layout,
+                        void* q_out, int64_t out_stride_token, int64_t out_stride_head, void* stream);
+
+/*
+ * mla_write_latent_paged and mla_write_latent_paged_fp8 with the rope position of each
+ * token given and either layout of the rope columns: the writes of drafted tokens, whose
+ * slots follow one another (token t of request b still goes to position cache_lengths[b] +
+ * (t - input_row_offsets[b])) while their rope positions are their depths in the tree.
+ *
+ * positions       [device] uint32 [total_tokens]: the freqs_cis row of each token; past the
+ *                 table: its last row
+ * rope_layout     mla_rope_layout_t; MLA_ROPE_HALF needs R % 16 == 0
+ * Other arguments, results, errors and validation order as in the calls without _at.
+ */
+mla_status_t mla_write_latent_paged_at(const void* kv_input, const uint32_t* input_row_offsets,
+                                       int32_t total_tokens, const uint32_t* positions,
+                                       const float* kv_norm_gamma, float epsilon, const float* freqs_cis,
+                                       int32_t max_seq_len, int32_t K, int32_t rope_layout,
+                                       const mla_paged_cache_t* cache, uint32_t layer_idx, void* stream);
+mla_status_t mla_write_latent_paged_fp8_at(const void* kv_input, const uint32_t* input_row_offsets,
+                                           int32_t total_tokens, const uint32_t* positions,
+                                           const float* kv_norm_gamma, float epsilon, const float* freqs_cis,
+                                           int32_t max_seq_len, int32_t K, int32_t rope_layout,
+                                           const mla_paged_cache_t* cache, const mla_cache_scales_t* cache_scales,
+                                           uint32_t layer_idx, void* stream);
+
+/*
+ * Attention of absorbed queries over the paged latent cache, for trees of drafted tokens
+ * (a decode step is the tree of one token, a chunk of a prompt the chain): the consumer of
+ * mla_absorb_q's q_latent and of the rows the latent write stored.
+ *
+ *   Request b has cached = cache_lengths[b] rows and n = input_row_offsets[b+1] -
+ *   input_row_offsets[b] drafted ones behind them, at positions cached + j.  Token i of
+ *   its n tokens (t = input_row_offsets[b] + i) sees every cached row, and drafted row j
+ *   if bit j % 64 of tree_mask[t][j / 64] is set (tree_mask NULL: if j <= i).
+ *     s_p             = scale * sum_c q_latent[t][h][c] * row_p[c]        (c < D_c, p seen)
+ *     out_latent[t][h][k] = sum_p exp(s_p) * row_p[k] / sum_p exp(s_p)    (k < K)
+ *     lse[t][h]       = ln sum_p exp(s_p)
+ *   A token that sees no row gets zeros and an lse of -infinity.  Scores, the running
+ *   maximum and sum, and the output sums are binary32; the weights exp(s_p - max) are
+ *   rounded to bf16 for the product with the rows on bf16 and e4m3 caches.  out_latent is
+ *   rounded once (round to nearest even).
+ *
+ * What a row that a token does not see holds (NaN and infinities included) does not change
+ * that token's output; neither does anything behind a request's last drafted row.
+ *
+ * q_latent        [device] [total_tokens][num_heads][D_c], D_c the cache's row width; bf16
+ *                 with a BF16 cache, float with an F32 cache
+ * input_row_offsets [device] uint32 [batch_size+1], [0] = 0, nondecreasing; rows of q_latent
+ *                 at or past input_row_offsets[batch_size] are neither read nor written to
+ * total_tokens    [host] T >= input_row_offsets[batch_size]
+ * num_heads       query heads, >= 1; T * num_heads * D_c < 2^31
+ * tree_mask       [device] uint64 [total_tokens][mask_words], 8-byte aligned, or NULL.
+ *                 Bits at or past n are ignored; drafted rows at or past 64 * mask_words are
+ *                 not seen.
+ * mask_words      >= 1 with a mask, 0 without; T * mask_words < 2^31
+ * scale           finite
+ * K               latent columns: K % 8 == 0, K <= 512; R = D_c - K: R % 8 == 0, R <= 512
+ * cache           [host] num_kv == 1, BF16 or F32, cache_lengths set.  Positions past the page
+ *                 table (max_pages_per_seq * page_size) are not seen; that product < 2^31.
+ * out_latent      [device] [total_tokens][num_heads][K] in q_latent's dtype, 16-byte aligned, written
+ * lse             [device] float [total_tokens][num_heads], 4-byte aligned, written; or NULL
+ * workspace       [device] >= mla_tree_attention_workspace_size(T, num_heads, K) bytes,
+ *                 256-byte aligned: partial results of requests that several workgroups
+ *                 share.  Nothing in it has to start at zero.  Calls that may overlap (other
+ *                 streams, captured graphs replayed side by side) need workspaces of their own.
+ * Rows of 576 columns with K = 512 on BF16 or e4m3 caches run on the matrix cores; other
+ * shapes and F32 run one wave per token and head.
+ */
+size_t mla_tree_attention_workspace_size(int32_t total_tokens, int32_t num_heads, int32_t K);
+mla_status_t mla_tree_attention_paged(const void* q_latent, const uint32_t* input_row_offsets,
+                                      int32_t total_tokens, int32_t num_heads, const uint64_t* tree_mask,
+                                      int32_t mask_words, float scale, int32_t K, const mla_paged_cache_t* cache,
+                                      uint32_t layer_idx, void* out_latent, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * mla_tree_attention_paged on an e4m3 cache: row_p[c] = code * scale of its block of 128
+ * columns.  The codes go into the products as they are (bf16 holds every e4m3 value); the
+ * scales multiply the scores' block sums and the weights, in binary32.
+ *
+ * q_latent, out_latent  bf16
+ * cache           dtype F8E4M3FN, D_c % 16 == 0
+ * cache_scales    [host] granularity 128, stride_token >= ceil(D_c / 128)
+ * Other arguments, limits and errors as in mla_tree_attention_paged.
+ */
+mla_status_t mla_tree_attention_paged_fp8_cache(const void* q_latent, const uint32_t* input_row_offsets,
+                                                int32_t total_tokens, int32_t num_heads,
+                                                const uint64_t* tree_mask, int32_t mask_words, float scale,
+                                                int32_t K, const mla_paged_cache_t* cache,
+                                                const mla_cache_scales_t* cache_scales, uint32_t layer_idx,
+                                                void* out_latent, float* lse, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/*
+ * Page upkeep: copying, forking, compacting and freeing pages of a paged cache, all layers
+ * and kv halves at once.  The four calls take any cache this library knows (BF16, F32, or
+ * F8E4M3FN with cache_scales; cache_scales is NULL for the others); all copies are bit
+ * copies, of the scales too.  Which page is free is the cache owner's bookkeeping: page ids
+ * are handed in, and freed ones handed back in a list.
+ *
+ * mla_copy_pages: page dst_pages[i] becomes a copy of page src_pages[i], i < count.
+ *   No destination may be the source of another pair or appear twice.  Pairs with an id
+ *   past the pool are skipped.
+ * src_pages, dst_pages  [device] uint32 [count]
+ */
+mla_status_t mla_copy_pages(const uint32_t* src_pages, const uint32_t* dst_pages, int32_t count,
+                            const mla_paged_cache_t* cache, const mla_cache_scales_t* cache_scales,
+                            void* stream);
+
+/*
+ * Fork requests: request children[i] becomes a copy of request parents[i] (rows of the
+ * page table), i < count, sharing its whole pages.
+ *
+ *   With L = cache_lengths[parent], full = L / page_size, part = L % page_size:
+ *     page_table[child][0:full] = page_table[parent][0:full], ref_counts of those pages + 1
+ *     if part > 0:  page_table[child][full] = new_pages[i], ref_counts[new_pages[i]] = 1,
+ *                   and the first `part` token rows of it, in every layer, are copied
+ *     cache_lengths[child] = L
+ *   Entries of the child's table row past these keep their values; with part == 0
+ *   new_pages[i] is not used and stays the caller's.  What the child held before must have
+ *   been freed.
+ *
+ * No child may be a parent in the same call, and no child or new page may appear twice.
+ * Pairs whose parent or child lies past the batch or that are equal, and pairs that need a
+ * new page and are given one past the pool, are skipped.  A length past the page table is
+ * taken as the table's.
+ *
+ * parents, children, new_pages  [device] uint32 [count]
+ * ref_counts      [device] uint32 [num_pages], updated: requests that hold each page
+ * cache           pages, page_table and cache_lengths are WRITTEN
+ */
+mla_status_t mla_fork_paged(const uint32_t* parents, const uint32_t* children, const uint32_t* new_pages,
+                            int32_t count, uint32_t* ref_counts, const mla_paged_cache_t* cache,
+                            const mla_cache_scales_t* cache_scales, void* stream);
+
+/*
+ * Free requests: every page that requests[i], i < count, holds (the first
+ * ceil(cache_lengths / page_size) entries of its table row) loses one reference; its
+ * entries become 0xFFFFFFFF and its length 0.  Pages left without references are appended
+ * to free_list at free_count[0], in ascending order of their ids, and free_count[0] grows
+ * by their number.
+ *
+ * A request that is listed twice is freed once; ids past the batch and entries past the
+ * pool are skipped; a page whose count is already 0 is left alone.  Entries that do not fit
+ * into the list (num_pages entries) are not stored, and free_count stops at num_pages.
+ *
+ * requests        [device] uint32 [count], count <= 65536
+ * ref_counts      [device] uint32 [num_pages], updated; counts below 2^31
+ * free_list       [device] uint32 [num_pages], entries from free_count[0] on are written
+ * free_count      [device] uint32 [1], updated
+ * cache           page_table and cache_lengths are WRITTEN; blocks may be NULL
+ */
+mla_status_t mla_free_paged(const uint32_t* requests, int32_t count, uint32_t* ref_counts, uint32_t* free_list,
+                            uint32_t* free_count, const mla_paged_cache_t* cache, void* stream);
+
+/*
+ * Move the rows of accepted drafted tokens together behind the cached ones: with c =
+ * accepted_offsets[b+1] - accepted_offsets[b] and a = accepted + accepted_offsets[b],
+ *   row at position cache_lengths[b] + i = row at position cache_lengths[b] + a[i],  i < c
+ * in every layer and kv half.  a[0] < a[1] < ... are positions in the request's drafted
+ * tokens (so a[i] >= i); rows of tokens that are not accepted are left as they are unless
+ * an accepted one takes their place.  cache_lengths is not updated.  Rows whose source or
+ * destination has no slot (past the page table, page id past the pool) are skipped.
+ * A page that is written must be the request's alone.
+ *
+ * accepted          [device] uint32 [total_accepted]
+ * accepted_offsets  [device] uint32 [batch_size+1], [0] = 0, nondecreasing
+ * total_accepted    [host] accepted_offsets[batch_size]
+ * cache             cache_lengths set; pages are WRITTEN
+ */
+mla_status_t mla_compact_paged(const uint32_t* accepted, const uint32_t* accepted_offsets, int32_t total_accepted,
+                               const mla_paged_cache_t* cache, const mla_cache_scales_t* cache_scales,
                                void* stream);
 
 /* Static text for a status code. */

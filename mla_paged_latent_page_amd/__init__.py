@@ -16,6 +16,11 @@ Entry points (same names as the C ABI):
   kv_matmul_paged              project hidden states and write them into K/V cache pages
   mla_gather_latent_paged      the gather step alone
   mla_latent_matmul            the up-projection step alone (rows already gathered)
+  mla_rope_freqs               a freqs_cis table, with long-context scaling
+  mla_rope_q                   rotation of every query head's rope columns at given positions
+  mla_write_latent_paged(_fp8)_at  the latent writes with the rope position of each token given
+  mla_tree_attention_paged(_fp8_cache)  attention of absorbed queries over cached and drafted rows
+  mla_copy_pages, mla_fork_paged, mla_free_paged, mla_compact_paged  page upkeep
   mla_check_indices            debug validation of index arrays (synchronous)
 """
 from __future__ import annotations
@@ -38,7 +43,12 @@ EXPORTS = ("mla_paged_cache_default_strides", "mla_decompress_k_paged", "mla_gat
            "kv_matmul_paged", "mla_check_indices", "mla_status_string", "mla_last_hip_error",
            "mla_abi_version", "mla_decompress_kv_paged", "mla_decompress_kv_paged_fp8",
            "mla_write_latent_paged", "mla_decompress_k_paged_fp8_cache", "mla_absorb_q", "mla_absorb_q_fp8",
-           "mla_write_latent_paged_fp8", "mla_decompress_kv_paged_fp8_cache", "mla_decompress_k_paged_fp8_noalloc")
+           "mla_write_latent_paged_fp8", "mla_decompress_kv_paged_fp8_cache", "mla_decompress_k_paged_fp8_noalloc",
+           "mla_rope_freqs", "mla_rope_q", "mla_write_latent_paged_at", "mla_write_latent_paged_fp8_at",
+           "mla_tree_attention_workspace_size", "mla_tree_attention_paged", "mla_tree_attention_paged_fp8_cache",
+           "mla_copy_pages", "mla_fork_paged", "mla_free_paged", "mla_compact_paged")
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 # mla_decompress_k_paged_fp8_noalloc's fixed device array (include/mla_paged.h)
 MLA_FP8_NOALLOC_SCRATCH_BYTES = 33 << 20
 
@@ -69,6 +79,15 @@ class ScalesDesc(ctypes.Structure):
         ("scales", ctypes.c_void_p), ("granularity", ctypes.c_uint32),
         ("stride_page", ctypes.c_int64), ("stride_layer", ctypes.c_int64),
         ("stride_kv", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+    ]
+
+
+class RopeParams(ctypes.Structure):
+    """Mirror of ``mla_rope_params_t``."""
+    _fields_ = [
+        ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double), ("scaling", ctypes.c_int32),
+        ("original_max_position", ctypes.c_int32),
     ]
 
 
@@ -122,6 +141,31 @@ def lib():
             L.mla_absorb_q.restype = i32
             L.mla_absorb_q_fp8.argtypes = [vp, i32, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp]
             L.mla_absorb_q_fp8.restype = i32
+            i64, f32 = ctypes.c_int64, ctypes.c_float
+            cd, sd = ctypes.POINTER(CacheDesc), ctypes.POINTER(ScalesDesc)
+            L.mla_rope_freqs.argtypes = [ctypes.POINTER(RopeParams), i32, i32, i32, vp, vp]
+            L.mla_rope_freqs.restype = i32
+            L.mla_rope_q.argtypes = [vp, i64, i64, i32, i32, i32, i32, i32, vp, vp, i32, i32, vp, i64, i64, vp]
+            L.mla_rope_q.restype = i32
+            L.mla_write_latent_paged_at.argtypes = [vp, vp, i32, vp, vp, f32, vp, i32, i32, i32, cd, u32, vp]
+            L.mla_write_latent_paged_at.restype = i32
+            L.mla_write_latent_paged_fp8_at.argtypes = [vp, vp, i32, vp, vp, f32, vp, i32, i32, i32, cd, sd, u32, vp]
+            L.mla_write_latent_paged_fp8_at.restype = i32
+            L.mla_tree_attention_workspace_size.argtypes = [i32, i32, i32]
+            L.mla_tree_attention_workspace_size.restype = sz
+            L.mla_tree_attention_paged.argtypes = [vp, vp, i32, i32, vp, i32, f32, i32, cd, u32, vp, vp, vp, sz, vp]
+            L.mla_tree_attention_paged.restype = i32
+            L.mla_tree_attention_paged_fp8_cache.argtypes = [vp, vp, i32, i32, vp, i32, f32, i32, cd, sd, u32, vp, vp,
+                                                             vp, sz, vp]
+            L.mla_tree_attention_paged_fp8_cache.restype = i32
+            L.mla_copy_pages.argtypes = [vp, vp, i32, cd, sd, vp]
+            L.mla_copy_pages.restype = i32
+            L.mla_fork_paged.argtypes = [vp, vp, vp, i32, vp, cd, sd, vp]
+            L.mla_fork_paged.restype = i32
+            L.mla_free_paged.argtypes = [vp, i32, vp, vp, vp, cd, vp]
+            L.mla_free_paged.restype = i32
+            L.mla_compact_paged.argtypes = [vp, vp, i32, cd, sd, vp]
+            L.mla_compact_paged.restype = i32
             L.kv_matmul_paged.argtypes = [vp, vp, i32, i32, vp, ctypes.POINTER(CacheDesc), u32, vp]
             L.kv_matmul_paged.restype = i32
             L.mla_gather_latent_paged.argtypes = [vp, vp, i32, ctypes.POINTER(CacheDesc), u32, vp, vp]
@@ -652,6 +696,222 @@ def kv_matmul_paged(hidden_state, input_row_offsets, weight, cache: PagedKVCache
     _gpu(hidden_state=hidden_state, input_row_offsets=input_row_offsets, weight=weight, **_cache_tensors(cache))
     st = lib().kv_matmul_paged(h, iro, T, Kd, w, ctypes.byref(desc), int(layer_idx), _stream(stream))
     _check(st, "kv_matmul_paged")
+
+
+def _rope_layout(layout):
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {', '.join(ROPE_LAYOUTS)}, not {layout!r}")
+    return ROPE_LAYOUTS[layout]
+
+
+def mla_rope_freqs(freqs_cis, theta: float = 10000.0, first_position: int = 0, scaling: str = "none",
+                   factor: float = 1.0, original_max_position: int = 0, beta_fast: float = 32.0,
+                   beta_slow: float = 1.0, amplitude: float = 1.0, stream=None) -> None:
+    """Fill freqs_cis[i] (a contiguous float32 [rows, d_rope] tensor) with amplitude * (cos, sin)
+    of (first_position + i) times each pair's frequency, scaled "none", "linear" or "by_parts"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, not {scaling!r}")
+    if freqs_cis is None or freqs_cis.dim() != 2:
+        raise ValueError("freqs_cis must be a [rows, d_rope] tensor")
+    rows, R = freqs_cis.shape
+    fr = _f32(freqs_cis, "freqs_cis", rows * R)
+    p = RopeParams(float(theta), float(factor), float(beta_fast), float(beta_slow), float(amplitude),
+                   ROPE_SCALINGS[scaling], int(original_max_position))
+    _gpu(freqs_cis=freqs_cis)
+    st = lib().mla_rope_freqs(ctypes.byref(p), int(first_position), rows, R, fr, _stream(stream))
+    _check(st, "mla_rope_freqs")
+
+
+def _freqs(freqs_cis):
+    if freqs_cis is None or freqs_cis.dim() != 2:
+        raise ValueError("freqs_cis must be a [max_seq_len, qk_rope_head_dim] tensor")
+    return _f32(freqs_cis, "freqs_cis", freqs_cis.shape[0] * freqs_cis.shape[1])
+
+
+def mla_rope_q(q, positions, freqs_cis, q_out, d_nope: int = 128, layout: str = "interleaved", stream=None) -> None:
+    """q_out[t, h] = q[t, h] with the columns from d_nope on rotated by freqs_cis[positions[t]].
+    q and q_out are [T, H, d_nope + d_rope] bfloat16 or float32 tensors with unit column stride;
+    passing q itself as q_out rotates in place."""
+    import torch
+    for t, name in ((q, "q"), (q_out, "q_out")):
+        if t is None or t.dim() != 3 or t.stride(2) != 1:
+            raise ValueError(f"{name} must be a [T, H, d_nope + d_rope] tensor with unit column stride")
+    if q.dtype not in (torch.bfloat16, torch.float32) or q_out.dtype != q.dtype:
+        raise ValueError("q and q_out must share a dtype, bfloat16 or float32")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    T, H, D = q.shape
+    lay = _rope_layout(layout)
+    fr = _freqs(freqs_cis)
+    if freqs_cis.shape[1] != D - d_nope:
+        raise ValueError("freqs_cis must be as wide as the rope part of q")
+    pos = _u32(positions, "positions", T)
+    _gpu(q=q, positions=positions, freqs_cis=freqs_cis, q_out=q_out)
+    dt = MLA_DTYPE_F32 if q.dtype == torch.float32 else MLA_DTYPE_BF16
+
+    def strides(t):   # the stride of a dimension of size 1 says nothing
+        head = t.stride(1) if H > 1 else D
+        return (t.stride(0) if T > 1 else H * head), head
+    st = lib().mla_rope_q(q.data_ptr(), *strides(q), T, H, int(d_nope), D - int(d_nope), dt, pos, fr,
+                          freqs_cis.shape[0], lay, q_out.data_ptr(), *strides(q_out), _stream(stream))
+    _check(st, "mla_rope_q")
+
+
+def mla_write_latent_paged_at(kv_input, input_row_offsets, positions, kv_norm_gamma, epsilon: float, freqs_cis,
+                              K: int, cache: PagedKVCache, layer_idx: int, layout: str = "interleaved",
+                              stream=None) -> None:
+    """mla_write_latent_paged with the rope position of each token given (drafted tokens:
+    their depth in the tree) and either layout of the rope columns."""
+    desc = _cache_desc(cache)
+    T, x, iro, g, fr, max_seq = _latent_write_args(kv_input, input_row_offsets, kv_norm_gamma, freqs_cis, K, desc)
+    pos = _u32(positions, "positions", T)
+    lay = _rope_layout(layout)
+    _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, positions=positions, kv_norm_gamma=kv_norm_gamma,
+         freqs_cis=freqs_cis, **_cache_tensors(cache))
+    st = lib().mla_write_latent_paged_at(x, iro, T, pos, g, float(epsilon), fr, int(max_seq), int(K), lay,
+                                         ctypes.byref(desc), int(layer_idx), _stream(stream))
+    _check(st, "mla_write_latent_paged_at")
+
+
+def mla_write_latent_paged_fp8_at(kv_input, input_row_offsets, positions, kv_norm_gamma, epsilon: float, freqs_cis,
+                                  K: int, cache: PagedKVCache, layer_idx: int, layout: str = "interleaved",
+                                  stream=None) -> None:
+    """mla_write_latent_paged_at into an e4m3 cache."""
+    desc, sdesc = _cache_desc(cache, scales=True)
+    T, x, iro, g, fr, max_seq = _latent_write_args(kv_input, input_row_offsets, kv_norm_gamma, freqs_cis, K, desc)
+    pos = _u32(positions, "positions", T)
+    lay = _rope_layout(layout)
+    _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, positions=positions, kv_norm_gamma=kv_norm_gamma,
+         freqs_cis=freqs_cis, **_cache_tensors(cache))
+    st = lib().mla_write_latent_paged_fp8_at(x, iro, T, pos, g, float(epsilon), fr, int(max_seq), int(K), lay,
+                                             ctypes.byref(desc), ctypes.byref(sdesc), int(layer_idx),
+                                             _stream(stream))
+    _check(st, "mla_write_latent_paged_fp8_at")
+
+
+def mla_tree_attention_workspace_size(total_tokens: int, num_heads: int, K: int = 512) -> int:
+    return int(lib().mla_tree_attention_workspace_size(int(total_tokens), int(num_heads), int(K)))
+
+
+def _attention_args(q_latent, input_row_offsets, tree_mask, K, desc, out_latent, lse, dtype):
+    import torch
+    if q_latent is None or q_latent.dim() != 3:
+        raise ValueError("q_latent must be a [T, H, D_c] tensor")
+    T, H, D = q_latent.shape
+    if D != desc.num_heads * desc.head_dim:
+        raise ValueError("q_latent rows must be as wide as the cache rows")
+    eb = 4 if dtype == torch.float32 else 2
+    q = _buf(q_latent, "q_latent", T * H * D * eb, (dtype,))
+    if out_latent is None or tuple(out_latent.shape) != (T, H, K):
+        raise ValueError(f"out_latent must be a [{T}, {H}, {K}] tensor")
+    out = _buf(out_latent, "out_latent", T * H * K * eb, (dtype,))
+    iro = _u32(input_row_offsets, "input_row_offsets", desc.batch_size + 1)
+    mask, words = None, 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.dtype not in (torch.int64, torch.uint64):
+            raise ValueError(f"tree_mask must be a 64-bit integer [{T}, mask_words] tensor")
+        words = tree_mask.shape[1]
+        mask = _buf(tree_mask, "tree_mask", T * words * 8)
+    ls = None
+    if lse is not None:
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse must be a [{T}, {H}] tensor")
+        ls = _f32(lse, "lse", T * H)
+    return T, H, q, iro, mask, words, out, ls
+
+
+def mla_tree_attention_paged(q_latent, input_row_offsets, tree_mask, scale: float, K: int, cache: PagedKVCache,
+                             layer_idx: int, out_latent, workspace, lse=None, stream=None) -> None:
+    """out_latent[t, h] = softmax(scale * q_latent[t, h] . rows) rows[:, :K] over the cached rows of the
+    token's request and the drafted rows behind them that tree_mask (64-bit words per token; None: the
+    tokens up to itself) names.  lse: optional float32 [T, H].  ``workspace``: a device tensor of at
+    least mla_tree_attention_workspace_size(T, H, K) bytes."""
+    import torch
+    desc = _cache_desc(cache)
+    dtype = torch.float32 if desc.dtype == MLA_DTYPE_F32 else torch.bfloat16
+    T, H, q, iro, mask, words, out, ls = _attention_args(q_latent, input_row_offsets, tree_mask, K, desc, out_latent,
+                                                         lse, dtype)
+    ws, ws_bytes = _workspace(workspace)
+    _gpu(q_latent=q_latent, input_row_offsets=input_row_offsets, tree_mask=tree_mask, out_latent=out_latent, lse=lse,
+         workspace=workspace, **_cache_tensors(cache))
+    st = lib().mla_tree_attention_paged(q, iro, T, H, mask, words, float(scale), int(K), ctypes.byref(desc),
+                                        int(layer_idx), out, ls, ws, ws_bytes, _stream(stream))
+    _check(st, "mla_tree_attention_paged")
+
+
+def mla_tree_attention_paged_fp8_cache(q_latent, input_row_offsets, tree_mask, scale: float, K: int,
+                                       cache: PagedKVCache, layer_idx: int, out_latent, workspace, lse=None,
+                                       stream=None) -> None:
+    """mla_tree_attention_paged over an e4m3 cache (codes times their block scales)."""
+    import torch
+    desc, sdesc = _cache_desc(cache, scales=True)
+    T, H, q, iro, mask, words, out, ls = _attention_args(q_latent, input_row_offsets, tree_mask, K, desc, out_latent,
+                                                         lse, torch.bfloat16)
+    ws, ws_bytes = _workspace(workspace)
+    _gpu(q_latent=q_latent, input_row_offsets=input_row_offsets, tree_mask=tree_mask, out_latent=out_latent, lse=lse,
+         workspace=workspace, **_cache_tensors(cache))
+    st = lib().mla_tree_attention_paged_fp8_cache(q, iro, T, H, mask, words, float(scale), int(K), ctypes.byref(desc),
+                                                  ctypes.byref(sdesc), int(layer_idx), out, ls, ws, ws_bytes,
+                                                  _stream(stream))
+    _check(st, "mla_tree_attention_paged_fp8_cache")
+
+
+def _page_descs(cache):
+    """The cache's descriptor, and the scale pool's where it has one."""
+    if cache.scales is None:
+        return _cache_desc(cache), None
+    desc, sdesc = _cache_desc(cache, scales=True)
+    return desc, ctypes.byref(sdesc)
+
+
+def mla_copy_pages(src_pages, dst_pages, cache: PagedKVCache, stream=None) -> None:
+    """Page dst_pages[i] becomes a copy of page src_pages[i], in every layer."""
+    desc, sdesc = _page_descs(cache)
+    n = src_pages.numel()
+    if dst_pages.numel() != n:
+        raise ValueError("src_pages and dst_pages must have the same number of entries")
+    src, dst = _u32(src_pages, "src_pages"), _u32(dst_pages, "dst_pages")
+    _gpu(src_pages=src_pages, dst_pages=dst_pages, **_cache_tensors(cache))
+    st = lib().mla_copy_pages(src, dst, n, ctypes.byref(desc), sdesc, _stream(stream))
+    _check(st, "mla_copy_pages")
+
+
+def mla_fork_paged(parents, children, new_pages, ref_counts, cache: PagedKVCache, stream=None) -> None:
+    """Request children[i] becomes a copy of request parents[i]: whole pages shared (ref_counts + 1),
+    the partly filled last page copied to new_pages[i]; writes the page table and the lengths."""
+    desc, sdesc = _page_descs(cache)
+    n = parents.numel()
+    if children.numel() != n or new_pages.numel() != n:
+        raise ValueError("parents, children and new_pages must have the same number of entries")
+    pa, ch, pg = _u32(parents, "parents"), _u32(children, "children"), _u32(new_pages, "new_pages")
+    refs = _u32(ref_counts, "ref_counts", desc.num_pages)
+    _gpu(parents=parents, children=children, new_pages=new_pages, ref_counts=ref_counts, **_cache_tensors(cache))
+    st = lib().mla_fork_paged(pa, ch, pg, n, refs, ctypes.byref(desc), sdesc, _stream(stream))
+    _check(st, "mla_fork_paged")
+
+
+def mla_free_paged(requests, ref_counts, free_list, free_count, cache: PagedKVCache, stream=None) -> None:
+    """Drop the listed requests' references; pages left without any are appended to free_list at
+    free_count[0] in ascending order.  Writes the page table and the lengths."""
+    desc, _ = _page_descs(cache)
+    req = _u32(requests, "requests")
+    refs = _u32(ref_counts, "ref_counts", desc.num_pages)
+    fl, fc = _u32(free_list, "free_list", desc.num_pages), _u32(free_count, "free_count", 1)
+    _gpu(requests=requests, ref_counts=ref_counts, free_list=free_list, free_count=free_count,
+         **_cache_tensors(cache))
+    st = lib().mla_free_paged(req, requests.numel(), refs, fl, fc, ctypes.byref(desc), _stream(stream))
+    _check(st, "mla_free_paged")
+
+
+def mla_compact_paged(accepted, accepted_offsets, cache: PagedKVCache, stream=None) -> None:
+    """Move the rows of each request's accepted drafted tokens (ascending positions in its draft)
+    together behind its cached rows, in every layer.  The lengths are not updated."""
+    desc, sdesc = _page_descs(cache)
+    acc = _u32(accepted, "accepted")
+    off = _u32(accepted_offsets, "accepted_offsets", desc.batch_size + 1)
+    _gpu(accepted=accepted, accepted_offsets=accepted_offsets, **_cache_tensors(cache))
+    st = lib().mla_compact_paged(acc, off, accepted.numel(), ctypes.byref(desc), sdesc, _stream(stream))
+    _check(st, "mla_compact_paged")
 
 
 def status_string(status: int) -> str:

@@ -28,7 +28,12 @@
 // 16 lanes (8 columns per lane), s = amax / 448 (1 for an all-zero block),
 // codes e4m3fn(y * (448 / amax)) rounded to nearest even; each lane stores
 // its 8 codes, the first lane of a block stores s into the scale pool.
-#include "launch.hpp"
+//
+// AT form (drafted tokens): the freqs_cis row comes from a position given per
+// token, the slot stays cache_lengths[b] + i; and the rope pairs may be columns
+// (j, j + R/2).  There lane l still produces columns 8l .. 8l+7: it reads its
+// own 8 columns and the 8 that are R/2 away, and their 8 (cos, sin) pairs.
+#include "step.hpp"
 
 namespace mla {
 namespace {
@@ -72,8 +77,13 @@ __device__ inline u32x2 codes8(const float (&y)[8], float to_codes)
             pack_e4m3x2(y[4] * to_codes, y[5] * to_codes) | (pack_e4m3x2(y[6] * to_codes, y[7] * to_codes) << 16)};
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(LatentWriteArgs a)
+template <bool AT>
+struct WriteArgs { using type = LatentWriteArgs; };
+template <>
+struct WriteArgs<true> { using type = LatentWriteAtArgs; };
+
+template <bool FP8, bool AT, bool HALF>
+__global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(typename WriteArgs<AT>::type a)
 {
     constexpr int TW = TOKENS_PER_WAVE;
     const int lane = threadIdx.x & 63;
@@ -83,15 +93,21 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(LatentWr
         return;
     const bool lat = lane * 8 < a.K;   // K <= 512: at most 64 lanes
     const bool rot = lane * 8 < a.R;   // R <= 512
+    // Half layout: which half the lane's columns are in, and its first pair.
+    const bool upper = HALF && lane * 16 >= a.R;
+    const int pair0 = HALF ? lane * 8 - (upper ? a.R / 2 : 0) : lane * 4;
 
     // Input rows of the wave's tokens (a tail wave re-reads its last token).
     u32x4 xv[TW], rv[TW];
+    [[maybe_unused]] u32x4 ov[TW];   // half layout: the columns R/2 away
 #pragma unroll
     for (int k = 0; k < TW; ++k) {
         const int t = min(t0 + k, a.T - 1);
         const char* src = reinterpret_cast<const char*>(a.X) + (int64_t)t * a.D * 2;
         xv[k] = lat ? ld16(src + lane * 16) : u32x4{0u, 0u, 0u, 0u};
         rv[k] = rot ? ld16(src + a.K * 2 + lane * 16) : u32x4{0u, 0u, 0u, 0u};
+        if constexpr (HALF)
+            ov[k] = rot ? ld16(src + a.K * 2 + lane * 16 + (upper ? -a.R : a.R)) : u32x4{0u, 0u, 0u, 0u};
     }
 
     // Request of each token: entries b < batch with input_row_offsets[b] <= t
@@ -119,17 +135,25 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(LatentWr
     // loaded before the first store.
     int64_t off[TW], soff[TW];
     f32x4 fr0[TW], fr1[TW];
+    [[maybe_unused]] f32x4 fr2[TW], fr3[TW];
 #pragma unroll
     for (int k = 0; k < TW; ++k) {
         const uint32_t t = (uint32_t)min(t0 + k, a.T - 1);
         const uint32_t b = cnt[k] == 0 ? 0u : min(cnt[k], a.L.batch) - 1;
         const uint32_t p = a.cache_len[b] + (t - a.iro[b]);
-        const uint32_t pf = p < (uint32_t)a.max_seq ? p : (uint32_t)a.max_seq - 1;   // freqs row, clamped
+        uint32_t pr = p;
+        if constexpr (AT)
+            pr = a.pos[t];
+        const uint32_t pf = pr < (uint32_t)a.max_seq ? pr : (uint32_t)a.max_seq - 1;   // freqs row, clamped
         off[k] = store_offset(a.L, b, p);   // -1: no slot for this position, nothing is stored
         soff[k] = FP8 ? store_offset(a.Ls, b, p) : 0;
-        const float* f = a.freqs + (int64_t)pf * a.R + lane * 8;
+        const float* f = a.freqs + (int64_t)pf * a.R + pair0 * 2;
         fr0[k] = rot ? *reinterpret_cast<const f32x4*>(f) : f32x4{0.f, 0.f, 0.f, 0.f};
         fr1[k] = rot ? *reinterpret_cast<const f32x4*>(f + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (HALF) {
+            fr2[k] = rot ? *reinterpret_cast<const f32x4*>(f + 8) : f32x4{0.f, 0.f, 0.f, 0.f};
+            fr3[k] = rot ? *reinterpret_cast<const f32x4*>(f + 12) : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
     }
     f32x4 g0 = {0.f, 0.f, 0.f, 0.f}, g1 = {0.f, 0.f, 0.f, 0.f};
     if (lat) {
@@ -167,13 +191,24 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(LatentWr
         // Rope part: 4 pairs per lane with the 4 (cos, sin) pairs of freqs_cis row p.
         float yr[8];
         {
-            const float cs[8] = {fr0[k][0], fr0[k][1], fr0[k][2], fr0[k][3], fr1[k][0], fr1[k][1], fr1[k][2], fr1[k][3]};
+            [[maybe_unused]] const float cs[8] = {fr0[k][0], fr0[k][1], fr0[k][2], fr0[k][3], fr1[k][0], fr1[k][1], fr1[k][2], fr1[k][3]};
+            if constexpr (!HALF) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x0 = bf16_lo(rv[k][i]), x1 = bf16_hi(rv[k][i]);
-                const float c = cs[2 * i], s = cs[2 * i + 1];
-                yr[2 * i] = rot ? x0 * c - x1 * s : 0.0f;
-                yr[2 * i + 1] = rot ? x0 * s + x1 * c : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    const float x0 = bf16_lo(rv[k][i]), x1 = bf16_hi(rv[k][i]);
+                    const float c = cs[2 * i], s = cs[2 * i + 1];
+                    yr[2 * i] = rot ? x0 * c - x1 * s : 0.0f;
+                    yr[2 * i + 1] = rot ? x0 * s + x1 * c : 0.0f;
+                }
+            } else {
+                const f32x4 fr[4] = {fr0[k], fr1[k], fr2[k], fr3[k]};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float c = fr[i / 2][2 * (i & 1)], s = fr[i / 2][2 * (i & 1) + 1];
+                    const float me = (i & 1) ? bf16_hi(rv[k][i / 2]) : bf16_lo(rv[k][i / 2]);
+                    const float other = (i & 1) ? bf16_hi(ov[k][i / 2]) : bf16_lo(ov[k][i / 2]);
+                    yr[i] = !rot ? 0.0f : upper ? other * s + me * c : me * c - other * s;
+                }
             }
         }
 
@@ -228,22 +263,36 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(LatentWr
 
 }  // namespace
 
-hipError_t launch_latent_write(const LatentWriteArgs& a, hipStream_t s)
+template <bool FP8, bool AT, bool HALF = false>
+static hipError_t launch(const typename WriteArgs<AT>::type& a, const char* name, hipStream_t s)
 {
     constexpr int per_block = WRITE_WAVES * TOKENS_PER_WAVE;
-    log_launch("latent_write_kernel<bf16>", (a.T + per_block - 1) / per_block, 64 * WRITE_WAVES, "T=%d K=%d R=%d", a.T, a.K, a.R);
-    hipLaunchKernelGGL(latent_write_kernel<false>, dim3((a.T + per_block - 1) / per_block), dim3(64 * WRITE_WAVES), 0, s,
-                       a);
+    const unsigned grid = (a.T + per_block - 1) / per_block;
+    log_launch(name, grid, 64 * WRITE_WAVES, "T=%d K=%d R=%d", a.T, a.K, a.R);
+    hipLaunchKernelGGL((latent_write_kernel<FP8, AT, HALF>), dim3(grid), dim3(64 * WRITE_WAVES), 0, s, a);
     return hipGetLastError();
+}
+
+hipError_t launch_latent_write(const LatentWriteArgs& a, hipStream_t s)
+{
+    return launch<false, false>(a, "latent_write_kernel<bf16>", s);
 }
 
 hipError_t launch_latent_write_fp8(const LatentWriteArgs& a, hipStream_t s)
 {
-    constexpr int per_block = WRITE_WAVES * TOKENS_PER_WAVE;
-    log_launch("latent_write_kernel<e4m3>", (a.T + per_block - 1) / per_block, 64 * WRITE_WAVES, "T=%d K=%d R=%d", a.T, a.K, a.R);
-    hipLaunchKernelGGL(latent_write_kernel<true>, dim3((a.T + per_block - 1) / per_block), dim3(64 * WRITE_WAVES), 0, s,
-                       a);
-    return hipGetLastError();
+    return launch<true, false>(a, "latent_write_kernel<e4m3>", s);
+}
+
+hipError_t launch_latent_write_at(const LatentWriteAtArgs& a, hipStream_t s)
+{
+    return a.half ? launch<false, true, true>(a, "latent_write_kernel<bf16, at, half>", s)
+                  : launch<false, true>(a, "latent_write_kernel<bf16, at>", s);
+}
+
+hipError_t launch_latent_write_fp8_at(const LatentWriteAtArgs& a, hipStream_t s)
+{
+    return a.half ? launch<true, true, true>(a, "latent_write_kernel<e4m3, at, half>", s)
+                  : launch<true, true>(a, "latent_write_kernel<e4m3, at>", s);
 }
 
 }  // namespace mla

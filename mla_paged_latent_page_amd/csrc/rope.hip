@@ -1,0 +1,190 @@
+// Rotary positions: freqs_cis tables and the rotation of query heads (page
+// "mla_prefill_decode_graph_fp8", Args freqs_cis, q).
+//
+// rope_freqs_kernel: entry (p, j) is (cos, sin) of p * g_j.  A position of 10^6
+// times a frequency of 1 has 20 bits before the binary point, so binary32 would
+// leave four for the angle: the product with g_j in quarter turns and its
+// reduction to [-1/2, 1/2] quarter turns are binary64 (three operations), and
+// only the reduced angle is rounded to binary32 (2^-26 quarter turns) for the
+// Taylor sums of sine and cosine, which stop below 2^-25 at pi/4.  Bound by its
+// stores.
+//
+// rope_q_kernel: one block per token (and 64 heads).  A thread keeps one group of
+// pairs of the rope part for every head it visits, so the token's (cos, sin) row is
+// read once into registers.  Bound by memory: the nope columns are only copied, in
+// 16-byte pieces that are all in flight before the first store.
+#include <algorithm>
+
+#include "step.hpp"
+
+namespace mla {
+namespace {
+
+__global__ void __launch_bounds__(256) rope_freqs_kernel(RopeFreqsArgs a)
+{
+    const int64_t total = (int64_t)a.rows * a.pairs;
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        const int row = (int)(i / a.pairs);
+        const int j = (int)(i - (int64_t)row * a.pairs);
+        const double turn = (double)((int64_t)a.first + row) * a.quarters[j];
+        const double n = rint(turn);
+        const float x = (float)(turn - n) * 1.57079632679489662f;
+        const int quadrant = (int)((int64_t)n & 3);
+        const float x2 = x * x;
+        const float sx = x + x * x2 * (-1.0f / 6 + x2 * (1.0f / 120 + x2 * (-1.0f / 5040 + x2 * (1.0f / 362880))));
+        const float cx = 1.0f + x2 * (-0.5f + x2 * (1.0f / 24 + x2 * (-1.0f / 720 + x2 * (1.0f / 40320 -
+                         x2 * (1.0f / 3628800)))));
+        const float s1 = (quadrant & 1) ? cx : sx, c1 = (quadrant & 1) ? sx : cx;
+        const float s = (quadrant & 2) ? -s1 : s1;
+        const float c = (quadrant == 1 || quadrant == 2) ? -c1 : c1;
+        *reinterpret_cast<f32x2*>(a.out + 2 * i) = f32x2{c * a.amplitude, s * a.amplitude};
+    }
+}
+
+// Rotate E elements (interleaved pairs) held in one 16-byte piece; cs holds their pairs.
+template <bool F32>
+__device__ inline u32x4 rotate_pairs(u32x4 v, const float* cs)
+{
+    u32x4 y;
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x0 = __uint_as_float(v[2 * i]), x1 = __uint_as_float(v[2 * i + 1]);
+            const float c = cs[2 * i], s = cs[2 * i + 1];
+            y[2 * i] = __float_as_uint(x0 * c - x1 * s);
+            y[2 * i + 1] = __float_as_uint(x0 * s + x1 * c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = bf16_lo(v[i]), x1 = bf16_hi(v[i]);
+            const float c = cs[2 * i], s = cs[2 * i + 1];
+            y[i] = pack_bf16x2(x0 * c - x1 * s, x0 * s + x1 * c);
+        }
+    }
+    return y;
+}
+
+// Rotate the pairs (element i of lo, element i of hi); cs holds one pair per element.
+template <bool F32>
+__device__ inline void rotate_halves(u32x4& lo, u32x4& hi, const float* cs)
+{
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = __uint_as_float(lo[i]), x1 = __uint_as_float(hi[i]);
+            const float c = cs[2 * i], s = cs[2 * i + 1];
+            lo[i] = __float_as_uint(x0 * c - x1 * s);
+            hi[i] = __float_as_uint(x0 * s + x1 * c);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a0 = bf16_lo(lo[i]), a1 = bf16_hi(lo[i]), b0 = bf16_lo(hi[i]), b1 = bf16_hi(hi[i]);
+            const float* t = cs + 4 * i;
+            lo[i] = pack_bf16x2(a0 * t[0] - b0 * t[1], a1 * t[2] - b1 * t[3]);
+            hi[i] = pack_bf16x2(a0 * t[1] + b0 * t[0], a1 * t[3] + b1 * t[2]);
+        }
+    }
+}
+
+constexpr int HEADS_PER_BLOCK = 64;
+
+template <bool F32, bool HALF>
+__global__ void __launch_bounds__(256) rope_q_kernel(RopeQArgs a)
+{
+    constexpr int E = F32 ? 4 : 8;             // elements of a 16-byte piece
+    constexpr int NCS = HALF ? 2 * E : E;      // table floats of a thread's pairs
+    const int t = blockIdx.x;
+    const int h0 = blockIdx.y * HEADS_PER_BLOCK;
+    const int nh = min(a.H - h0, HEADS_PER_BLOCK);
+    const char* q = a.q + (int64_t)t * a.q_st + (int64_t)h0 * a.q_sh;
+    char* out = a.out + (int64_t)t * a.o_st + (int64_t)h0 * a.o_sh;
+    const uint32_t p0 = a.pos[t];
+    const uint32_t p = p0 < (uint32_t)a.max_seq ? p0 : (uint32_t)a.max_seq - 1;
+
+    // Rope part: `units` pieces (pairs of pieces in the half layout) per head.
+    const int units = a.R / (HALF ? 2 * E : E);
+    const int per_pass = 256 / units;          // heads the block covers at once (units <= 128)
+    const int g = threadIdx.x % units;
+    const int hh = threadIdx.x / units;
+    constexpr int U = 4;
+    if (hh < per_pass && hh < nh) {
+        float cs[NCS];
+        const float* f = a.freqs + (int64_t)p * a.R + g * NCS;
+#pragma unroll
+        for (int i = 0; i < NCS / 4; ++i) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(f + 4 * i);
+            cs[4 * i] = v[0], cs[4 * i + 1] = v[1], cs[4 * i + 2] = v[2], cs[4 * i + 3] = v[3];
+        }
+        const int at = a.nope_bytes + g * 16;
+        const int hi_at = a.R * (16 / E) / 2;   // bytes between the halves
+        for (int h = hh; h < nh; h += U * per_pass) {
+            u32x4 v[U], w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hu = min(h + u * per_pass, nh - 1);
+                v[u] = ld16(q + (int64_t)hu * a.q_sh + at);
+                if constexpr (HALF)
+                    w[u] = ld16(q + (int64_t)hu * a.q_sh + at + hi_at);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int hu = h + u * per_pass;
+                if (hu < nh) {
+                    char* o = out + (int64_t)hu * a.o_sh + at;
+                    if constexpr (HALF) {
+                        rotate_halves<F32>(v[u], w[u], cs);
+                        st16(o, v[u]);
+                        st16(o + hi_at, w[u]);
+                    } else {
+                        st16(o, rotate_pairs<F32>(v[u], cs));
+                    }
+                }
+            }
+        }
+    }
+    if (!a.copy)
+        return;
+    const uint32_t pieces = (uint32_t)a.nope_bytes / 16;
+    const uint32_t total = pieces * (uint32_t)nh;
+    for (uint32_t i = threadIdx.x; i < total; i += U * 256) {
+        u32x4 v[U];
+        int64_t o[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t k = min(i + u * 256, total - 1);
+            const uint32_t h = k / pieces, c = k - h * pieces;
+            v[u] = ld16(q + (int64_t)h * a.q_sh + c * 16);
+            o[u] = (int64_t)h * a.o_sh + c * 16;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * 256 < total)
+                st16(out + o[u], v[u]);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rope_freqs(const RopeFreqsArgs& a, hipStream_t s)
+{
+    const int64_t total = (int64_t)a.rows * a.pairs;
+    const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 256 * 16);
+    log_launch("rope_freqs_kernel", grid, 256, "rows=%d pairs=%d", a.rows, a.pairs);
+    hipLaunchKernelGGL(rope_freqs_kernel, dim3(grid), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_rope_q(const RopeQArgs& a, bool f32, bool half, hipStream_t s)
+{
+    const dim3 grid(a.T, (a.H + HEADS_PER_BLOCK - 1) / HEADS_PER_BLOCK);
+    log_launch("rope_q_kernel", grid.x * grid.y, 256, "T=%d H=%d R=%d f32=%d half=%d", a.T, a.H, a.R, f32, half);
+    auto* kernel = f32 ? (half ? rope_q_kernel<true, true> : rope_q_kernel<true, false>)
+                       : (half ? rope_q_kernel<false, true> : rope_q_kernel<false, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace mla
