@@ -78,7 +78,7 @@ hipError_t launch_latent_write_at(const LatentWriteAtArgs& a, hipStream_t s);
 hipError_t launch_latent_write_fp8_at(const LatentWriteAtArgs& a, hipStream_t s);
 // Matrix-core form (576-column rows, K = 512), and whether it takes a call.
 bool tree_attention_mfma_fits(const TreeAttentionArgs& a, AttnKind kind);
-hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, hipStream_t s);
+hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind, hipStream_t s);
 hipError_t launch_tree_attention(const TreeAttentionArgs& a, AttnKind kind, hipStream_t s);
 hipError_t launch_copy_pages(const PageArgs& a, hipStream_t s);
 hipError_t launch_fork(const PageArgs& a, hipStream_t s);

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256) tree_attention_general(TreeAttentionArgs 
 hipError_t launch_tree_attention(const TreeAttentionArgs& a, AttnKind kind, hipStream_t s)
 {
     if (tree_attention_mfma_fits(a, kind))
-        return launch_tree_attention_mfma(a, s);
+        return launch_tree_attention_mfma(a, kind, s);
     const dim3 grid((unsigned)a.T * ((a.H + 3) / 4));
     log_launch("tree_attention_general", grid.x, 256, "T=%d H=%d K=%d D=%d kind=%d", a.T, a.H, a.K, a.D, (int)kind);
     if (kind == ATTN_F32)

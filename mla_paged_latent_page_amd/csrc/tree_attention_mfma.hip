@@ -1,6 +1,7 @@
-// Tree attention on the matrix cores: rows of 576 columns (512 latent + 64 rope),
-// bf16 cache (see tree_attention.hip for the operator and the general form).
+// Tree attention on the matrix cores: rows of 576 columns (512 latent + 64 rope), bf16 or
+// e4m3 cache (see tree_attention.hip for the operator and the general form).
 #include <algorithm>
+#include <utility>
 
 #include "step.hpp"
 
@@ -14,13 +15,36 @@ constexpr int BLOCK_BYTES = TILE * 128;
 constexpr int STAGE = BLOCKS * BLOCK_BYTES;  // 36,864 bytes
 constexpr int STAGES = 4;
 constexpr int WAVES = 4;
-constexpr int LOADS = BLOCKS;                // LDS loads per wave and tile
+// e4m3: a tile stays in codes, 4 blocks of 32 rows x 128 codes and one of 32 x 64, with its
+// scales behind the four stages; then the query fragments for which the conversion leaves no
+// registers.
+constexpr int STAGE8 = TILE * D;
+constexpr int SCALES_WAVE = 256;             // 5 blocks x 8 rows, floats
+constexpr int SCALES = WAVES * SCALES_WAVE;
+constexpr int SCALES_AT = STAGES * STAGE8;
+constexpr int QUERY_AT = SCALES_AT + STAGES * SCALES;
+constexpr int QUERY_KEPT = 15;               // fragments in registers; the others are in LDS
+constexpr int QUERY_WAVE = (D / 16 - QUERY_KEPT) * 1024;
+constexpr int SMEM8 = QUERY_AT + WAVES * QUERY_WAVE;
+static_assert(SMEM8 <= 163840 && STAGES * STAGE <= 163840, "LDS");
 constexpr int PIECE_WAVE = 32 * (K + 2);     // floats of one wave's partial result: 32 rows, maximum, sum
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kSlack = 8.0f;               // the reference maximum may lag by 2^8
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+// f(0), f(1), ..., f(N - 1) with constant arguments.
+template <class F, int... I>
+__device__ __attribute__((always_inline)) inline void each(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __attribute__((always_inline)) inline void each(F&& f)
+{
+    each(f, std::make_integer_sequence<int, N>{});
+}
 
 struct MfmaParams {
     TreeAttentionArgs a;
@@ -151,6 +175,12 @@ struct Schedule {
     }
 };
 
+typedef int v2i32 __attribute__((ext_vector_type(2)));
+__device__ inline u32x2 lds_tr8(const char* p)
+{
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                         (__attribute__((address_space(3))) v2i32*)(__attribute__((address_space(3))) void*)p));
+}
 __device__ inline v4i16 lds_tr16(const char* p)
 {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -165,21 +195,48 @@ __device__ inline float swap32(float v)
     return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-// 16 bytes per lane into LDS at lds + 16 * lane, by all lanes or (on = 0, else ~0) none: from a
-// uniform base and a 32-bit lane offset, or from a lane address.
-__device__ inline void load_lds(const char* base, uint32_t voff, uint32_t lds, uint32_t on)
+// 16 (or 4) bytes per lane into LDS at lds + 16 (4) * lane, by the lanes of the masks lo and
+// hi: from a uniform base and a 32-bit lane offset, or from a lane address.
+__device__ inline void load_lds(const char* base, uint32_t voff, uint32_t lds, uint32_t lo, uint32_t hi)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\t"
+                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
                  :
-                 : "s"(lds), "v"(voff), "s"(base), "s"(on)
+                 : "s"(lds), "v"(voff), "s"(base), "s"(lo), "s"(hi)
                  : "memory", "m0");
 }
-__device__ inline void load_lds(const char* src, uint32_t lds, uint32_t on)
+__device__ inline void load_lds(const char* src, uint32_t lds, uint32_t lo, uint32_t hi)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1"
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\t"
+                 "global_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1"
                  :
-                 : "s"(lds), "v"(src), "s"(on)
+                 : "s"(lds), "v"(src), "s"(lo), "s"(hi)
                  : "memory", "m0");
+}
+__device__ inline void load_lds4(const char* base, uint32_t voff, uint32_t lds, uint32_t lo, uint32_t hi)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\t"
+                 "global_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1"
+                 :
+                 : "s"(lds), "v"(voff), "s"(base), "s"(lo), "s"(hi)
+                 : "memory", "m0");
+}
+__device__ inline void load_lds4(const char* src, uint32_t lds, uint32_t lo, uint32_t hi)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\t"
+                 "global_load_lds_dword %1, off\n\ts_mov_b64 exec, -1"
+                 :
+                 : "s"(lds), "v"(src), "s"(lo), "s"(hi)
+                 : "memory", "m0");
+}
+
+// The lane's number, worked out where it is needed (it and what is derived from it would
+// otherwise hold registers through the whole kernel).
+__device__ inline uint32_t lane_again()
+{
+    uint32_t x;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+    return x;
 }
 
 template <int N>
@@ -190,19 +247,20 @@ __device__ inline void wait_loads()
 
 // One product with its sums in ordinary registers: the output sums take all 256 accumulation
 // registers, and the compiler would put these there too.  It does not see that this is a matrix
-// instruction, so the last one of a chain waits for its result before anything can read it
-// (12 wait states after 8 passes; back-to-back products into the same registers need none).
+// instruction, so each waits two states for operands just written by vector instructions, and
+// the last one of a chain for its result before anything can read it (12 wait states after 8
+// passes; back-to-back products into the same registers need none).
 __device__ inline void mfma_first(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
 }
 __device__ inline void mfma_next(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
 }
 __device__ inline void mfma_last(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
+    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
 }
 
 // Element e of an output sum times f, in its accumulation register (written out, as the
@@ -215,6 +273,19 @@ __device__ inline void scale_sum(f32x16& o, int e, float f)
         : "v"(f));
     o[e] = x;
 }
+
+// Eight e4m3 codes as bf16 (every code's value is one).
+__device__ inline bf16x8 bf16_of_codes(u32x2 v)
+{
+    auto two = [](uint32_t x, auto high) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, decltype(high)::value));
+    };
+    const std::false_type lo;
+    const std::true_type hi;
+    return as_bf16x8(u32x4{two(v[0], lo), two(v[0], hi), two(v[1], lo), two(v[1], hi)});
+}
+
+__device__ inline bf16x8 bf16_of_codes(bf16x8 v) { return v; }
 
 __device__ inline bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
@@ -237,10 +308,11 @@ __device__ inline void store_row(uint16_t* out, const f32x16 (&o)[16], float inv
         }
 }
 
-template <bool PAGE8>
+template <bool PAGE8, bool FP8>
 __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams P)
 {
-    __shared__ __attribute__((aligned(1024))) char smem[STAGES * STAGE];
+    __shared__ __attribute__((aligned(1024))) char smem[FP8 ? SMEM8 : STAGES * STAGE];
+    constexpr int LOADS = FP8 ? 6 : BLOCKS;   // LDS loads per wave and tile
     const TreeAttentionArgs& a = P.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -259,27 +331,36 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         stop = uniform(sched.cut(w + 1, r));
     uint32_t u = uniform(sched.cut(w, r));
 
-    // Lane-constant offsets.  A tile is stored as 9 blocks of 32 rows x 128 bytes; the
-    // 16-byte granule g of row x sits at g ^ f(x), where bits 2, 1 and 0 of f(x) are bits 1, 2
-    // and 3 of x: 16 rows of the 16-byte reads (two rows fill the 256 bytes of all banks) and
-    // 4 rows x 64 bytes of the transposing reads then fall on different banks.
-    auto f = [](uint32_t x) { return (x >> 1 & 1) << 2 | (x >> 2 & 1) << 1 | (x >> 3 & 1); };
-    const uint32_t load_off = (((uint32_t)lane & 7) ^ f(wave * 8 + (lane >> 3))) * 16;
+    // Lane-constant offsets.  A tile is stored in blocks of 32 rows x 128 bytes (64 bf16 columns
+    // or 128 codes); the 16-byte granule g of row x sits at g ^ f(x), f(x) a permutation of bits
+    // 1 to 3 of x.  (Two rows fill the 256 bytes of all banks.)  bf16: 16 rows of the 16-byte
+    // reads, and 4 rows x 64 bytes of the transposing reads, fall on different banks.  e4m3:
+    // 8 rows x 32 bytes of the transposing reads do; the 8-byte reads of all 32 rows touch each
+    // bank twice.  In the last 64 codes of a row granule g sits at g ^ (x / 4) % 4.
+    auto f = [](uint32_t x) {
+        return FP8 ? (x >> 1 & 1) << 2 | (x >> 3 & 1) << 1 | (x >> 2 & 1) : (x >> 1 & 1) << 2 | (x >> 2 & 1) << 1 | (x >> 3 & 1);
+    };
     const uint32_t fk = f(col);
+    // Score operands: bf16: granules 2 s + half of a block, s = 0 .. 3; e4m3: bytes 8 half of
+    // granule 0 (others by exclusive or).
     uint32_t k_off[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-        k_off[s] = col * 128 + (((2 * s + half) ^ fk) * 16);
-    // Transposing reads: lane c of a 16-lane group addresses row c / 4 and 8 bytes of columns.
-    const uint32_t c16 = lane & 15, vrow = 4 * half + (c16 >> 2);
-    uint32_t v_off[2][2];   // [feature block parity][rows vrow or vrow + 8]
+        k_off[s] = FP8 ? (s == 0 ? col * 128 + fk * 16 : col * 64 + (col >> 2 & 3) * 16) + half * 8 : col * 128 + (((2 * s + half) ^ fk) * 16);
+    // Transposing reads.  bf16: lane c of a 16-lane group addresses row c / 4 and 8 bytes of its
+    // columns; e4m3: row c / 2 of the eight (rows 0 .. 3 and 8 .. 11, + 4 half) and 8 codes.
+    const uint32_t c16 = lane & 15, vrow = 4 * half + (FP8 ? (c16 >> 1 & 3) + 8 * (c16 >> 3) : c16 >> 2);
+    uint32_t v_off[2][2];   // bf16: [feature block parity][rows vrow or vrow + 8]; e4m3: [0][0]
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            v_off[s][h] = (vrow + 8 * h) * 128 + (c16 & 1) * 8 +
-                          (((uint32_t)(4 * s + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ f(vrow + 8 * h)) * 16);
-    const uint32_t lds0 = lds_addr(smem) + wave * 1024;
+            v_off[s][h] = FP8 ? vrow * 128 + (c16 & 1) * 8 + (((uint32_t)(lane >> 4 & 1) ^ f(vrow)) * 16)
+                              : (vrow + 8 * h) * 128 + (c16 & 1) * 8 +
+                                    (((uint32_t)(4 * s + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ f(vrow + 8 * h)) * 16);
+    const uint32_t lds0 = lds_addr(smem);
+    // Stage of tile t (the tiles of an item counted from 0).
+    auto stage_of = [](uint32_t t) __attribute__((always_inline)) { return (t & (STAGES - 1)) * (FP8 ? STAGE8 : STAGE); };
     const float c = a.scale * kLog2e;
 
     while (u < stop) {
@@ -306,12 +387,26 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         const uint32_t tok = min(row, rows - 1) / (uint32_t)a.H;   // token of the request
 
         // Query fragments: lane holds features 16 s + 8 half .. + 7 of its row.
-        bf16x8 q[D / 16];
+        constexpr int KEPT = FP8 ? QUERY_KEPT : D / 16;
+        bf16x8 q[KEPT];
+        char* my_q = FP8 ? smem + QUERY_AT + wave * QUERY_WAVE + lane * 16 : nullptr;
         {
             const char* src = static_cast<const char*>(a.q) + (int64_t)qrow * (D * 2) + half * 16;
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
+            for (int s = 0; s < KEPT; ++s)
                 q[s] = as_bf16x8(ld16(src + s * 32));
+            if constexpr (FP8) {
+#pragma unroll
+                for (int s0 = KEPT; s0 < D / 16; s0 += 7) {
+                    u32x4 v[7];
+#pragma unroll
+                    for (int s = 0; s < 7; ++s)
+                        v[s] = ld16(src + (s0 + s) * 32);
+#pragma unroll
+                    for (int s = 0; s < 7; ++s)
+                        lds_st16(my_q + (s0 + s - KEPT) * 1024, v[s]);
+                }
+            }
         }
         // The stages of the item before are no longer read (and no load into them is in flight:
         // the last step waited for all of them, and those behind the last tile are switched off).
@@ -336,35 +431,70 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             return *(const __attribute__((address_space(4))) uint32_t*)(uint64_t)entry;
         };
 
-        // Where the loads of a tile come from and go to; then its 9 loads one by one: spread over
+        // Where the loads of a tile come from and go to; then its loads one by one: spread over
         // a step they never wait for one another (64 bytes per clock and CU).
         const char* src_base = nullptr;     // PAGE8: uniform; else the lane's address
-        uint32_t src_off = 0, dst = 0, src_on = 0;
+        const char* scale_src = nullptr;
+        uint32_t src_off = 0, src_off4 = 0, scale_off = 0, dst = 0, scale_dst = 0, src_on = 0;
+        [[maybe_unused]] const char* src_base4 = nullptr;
         uint32_t last_tile = n_tiles;
         asm("" : "+s"(last_tile));   // the switch below stays scalar arithmetic
         auto locate = [&](uint32_t t) __attribute__((always_inline)) {
-            dst = (t & (STAGES - 1)) * STAGE + lds0;
             src_on = (uint32_t)((int32_t)(t - last_tile) >> 31);   // all ones while t < n_tiles
+            dst = lds0 + stage_of(t) + wave * 1024;
+            const uint32_t ln = lane_again();
+            const uint32_t load_off = ((ln & 7) ^ f(wave * 8 + (ln >> 3))) * 16;
+            [[maybe_unused]] const uint32_t load_off4 = 512 + ((ln ^ (2 * wave + (ln >> 4))) & 3) * 16;
             if constexpr (PAGE8) {
                 const uint32_t pg = group_start(t);
                 const uint32_t slot = pg - (__umulhi(pg, P.ps_magic) >> P.ps_shift) * a.L.page_size;
-                src_base = a.L.base + (int64_t)min(next_id, a.L.num_pages - 1) * a.L.stride_page +
-                           (int64_t)slot * a.L.stride_token;
+                const uint32_t id = min(next_id, a.L.num_pages - 1);
+                src_base = a.L.base + (int64_t)id * a.L.stride_page + (int64_t)slot * a.L.stride_token;
                 const uint32_t last = len - 1 - pg;
-                src_off = min((uint32_t)lane >> 3, last) * (uint32_t)a.L.stride_token + load_off;
+                src_off = min(ln >> 3, last) * (uint32_t)a.L.stride_token + load_off;
+                if constexpr (FP8) {
+                    src_off4 = min(ln >> 2, last) * (uint32_t)a.L.stride_token + load_off4;
+                    scale_src = a.Ls.base + (int64_t)id * a.Ls.stride_page + (int64_t)slot * a.Ls.stride_token;
+                    scale_off = min(ln & 7, last) * (uint32_t)a.Ls.stride_token + (ln >> 3) * 4;
+                }
             } else {
-                const uint32_t p = min((tile0 + t) * TILE + wave * 8 + ((uint32_t)lane >> 3), len - 1);
-                const uint32_t lp = p / a.L.page_size;
-                const uint32_t id = min(a.L.page_table[table_row + min(lp, a.L.max_pages - 1)], a.L.num_pages - 1);
-                src_base = a.L.base + (int64_t)id * a.L.stride_page +
-                           (int64_t)(p - lp * a.L.page_size) * a.L.stride_token + load_off;
+                auto at = [&](const PagedLayer& L, uint32_t row) __attribute__((always_inline)) {
+                    const uint32_t p = min((tile0 + t) * TILE + wave * 8 + row, len - 1);
+                    const uint32_t lp = p / L.page_size;
+                    const uint32_t id = min(L.page_table[table_row + min(lp, L.max_pages - 1)], L.num_pages - 1);
+                    return L.base + (int64_t)id * L.stride_page + (int64_t)(p - lp * L.page_size) * L.stride_token;
+                };
+                src_base = at(a.L, ln >> 3) + load_off;
+                if constexpr (FP8) {
+                    src_base4 = at(a.L, (ln >> 2) & 7) + load_off4;
+                    scale_src = at(a.Ls, ln & 7) + (ln >> 3) * 4;
+                }
             }
+            if constexpr (FP8)
+                scale_dst = lds0 + SCALES_AT + (t & (STAGES - 1)) * SCALES + wave * SCALES_WAVE;
         };
         auto load = [&](int j) __attribute__((always_inline)) {
+            if constexpr (FP8) {
+                if (j == 5) {         // lane l: scale of block l / 8 of row l % 8
+                    if constexpr (PAGE8)
+                        load_lds4(scale_src, scale_off, scale_dst, src_on, src_on & 0xFFu);
+                    else
+                        load_lds4(scale_src, scale_dst, src_on, src_on & 0xFFu);
+                    return;
+                }
+                if (j == 4) {         // lanes 0 .. 31: the last 64 codes of row l / 4
+                    const uint32_t to = dst - wave * 512 + 4 * BLOCK_BYTES;
+                    if constexpr (PAGE8)
+                        load_lds(src_base, src_off4, to, src_on, 0);
+                    else
+                        load_lds(src_base4, to, src_on, 0);
+                    return;
+                }
+            }
             if constexpr (PAGE8)
-                load_lds(src_base, src_off + j * 128, dst + j * BLOCK_BYTES, src_on);
+                load_lds(src_base, src_off + j * 128, dst + j * BLOCK_BYTES, src_on, src_on);
             else
-                load_lds(src_base + j * 128, dst + j * BLOCK_BYTES, src_on);
+                load_lds(src_base + j * 128, dst + j * BLOCK_BYTES, src_on, src_on);
         };
         auto issue = [&](uint32_t t) __attribute__((always_inline)) {
             locate(t);
@@ -372,25 +502,32 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             for (int j = 0; j < LOADS; ++j)
                 load(j);
         };
+        // e4m3: scales of block b of the rows 8 i + 4 half .. + 3 of a tile.
+        auto scales_at = [&](uint32_t t) __attribute__((always_inline)) {
+            return SCALES_AT + (t & (STAGES - 1)) * SCALES + (lane_again() >> 5) * 16;
+        };
+        auto scales_of = [&](uint32_t at, int b, int i) __attribute__((always_inline)) {
+            return *reinterpret_cast<const f32x4*>(smem + at + i * SCALES_WAVE + b * 32);
+        };
 
+        uint32_t id2 = 0, id3 = 0;
         if constexpr (PAGE8) {
-            const uint32_t id0 = id_at(entry_of(0)), id1 = id_at(entry_of(1)), id2 = id_at(entry_of(2)),
-                           id3 = id_at(entry_of(3));
+            const uint32_t id0 = id_at(entry_of(0)), id1 = id_at(entry_of(1));
+            id2 = id_at(entry_of(2));
+            id3 = id_at(entry_of(3));
             next_id = id0;
             issue(0);
             next_id = id1;
-            issue(1);
-            next_id = id2;
-            issue(2);
-            next_id = id3;
         } else {
             issue(0);
-            issue(1);
-            issue(2);
         }
+        issue(1);
+        next_id = id2;
+        issue(2);
+        next_id = id3;
 
-        // Start of step t: tile t + 1 has landed for every wave and every wave is done with
-        // tile t - 1, whose stage takes tile t + 3.
+        // Start of step t: tile t + 1 is there for every wave and every wave is done with tile
+        // t - 1, whose stage takes tile t + 3.
         auto enter = [&](uint32_t t) __attribute__((always_inline)) {
             if (t + 2 < n_tiles)
                 wait_loads<LOADS>();
@@ -404,17 +541,26 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 // Drafted rows may be hidden from some tokens and hold anything: a weight of 0
                 // would turn their infinities and NaN into NaN, so those become 0 here (a token
                 // that sees such a row has a NaN weight for it already).
-                char* mine = smem + (t & (STAGES - 1)) * STAGE + wave * 1024 + lane * 16;
+                char* mine = smem + stage_of(t) + wave * 1024 + lane * 16;
                 if (p0 + wave * 8 + (lane >> 3) >= cached)
-                    for (int j = 0; j < BLOCKS - 1; ++j) {
+                    for (int j = 0; j < K / (FP8 ? 128 : 64); ++j) {
                         u32x4 v = lds_ld16(mine + j * BLOCK_BYTES);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            v[e] = nonfinite16(v[e]) ? v[e] & 0xFFFF0000u : v[e];
-                            v[e] = nonfinite16(v[e] >> 16) ? v[e] & 0xFFFFu : v[e];
+                            if constexpr (FP8) {   // bytes of 0x7F or 0xFF
+                                const uint32_t nan = ((v[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                v[e] &= ~((nan >> 7) * 0xFFu);
+                            } else {
+                                v[e] = nonfinite16(v[e]) ? v[e] & 0xFFFF0000u : v[e];
+                                v[e] = nonfinite16(v[e] >> 16) ? v[e] & 0xFFFFu : v[e];
+                            }
                         }
                         lds_st16(mine + j * BLOCK_BYTES, v);
                     }
+                if (FP8 && lane < 40 && p0 + wave * 8 + (lane & 7) >= cached) {
+                    float* sc = reinterpret_cast<float*>(smem + SCALES_AT + (t & (STAGES - 1)) * SCALES + wave * SCALES_WAVE) + lane;
+                    *sc = fabsf(*sc) < INFINITY ? *sc : 0.0f;
+                }
                 lds_barrier();
             }
         };
@@ -470,32 +616,77 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 
         // Scores of tile t: lane (col, half) gets rows 8 (i / 4) + 4 half + i % 4 for its query.
         // Fragments are read KD products ahead; `between(k)` is other work during product k.
-        constexpr int KN = D / 16, KD = 6, VN = 2 * (K / 32), VD = 4;
+        // e4m3: codes become bf16 on the way to the matrix cores, one product ahead; each block
+        // of 128 columns has sums of its own, times the block's scale of each row.
+        constexpr int KN = D / 16, KD = FP8 ? 5 : 6, VN = 2 * (K / 32), VD = 4;
+        using Frag = std::conditional_t<FP8, u32x2, bf16x8>;
         auto scores = [&](uint32_t t, auto between) __attribute__((always_inline)) {
-            const char* st = smem + (t & (STAGES - 1)) * STAGE;
-            auto frag = [&](int k) __attribute__((always_inline)) {
-                return as_bf16x8(lds_ld16(st + k_off[k & 3] + (k >> 2) * BLOCK_BYTES));
+            const char* st = smem + stage_of(t);
+            // Exclusive or of the granule after the sum with the stage: it is not worth keeping.
+            [[maybe_unused]] const uint32_t at8[2] = {stage_of(t) + k_off[0], stage_of(t) + k_off[1]};
+            auto frag = [&](int k) __attribute__((always_inline)) -> Frag {
+                if constexpr (FP8)
+                    return *reinterpret_cast<const u32x2*>(
+                        smem + (at8[k >> 5] ^ ((k < 32 ? k & 7 : k & 3) * 16)) + (k >> 3) * BLOCK_BYTES);
+                else
+                    return as_bf16x8(lds_ld16(st + k_off[k & 3] + (k >> 2) * BLOCK_BYTES));
             };
-            f32x16 acc;
-            bf16x8 kf[KD];
+            auto query = [&](int k) __attribute__((always_inline)) { return as_bf16x8(lds_ld16(my_q + (k - KEPT) * 1024)); };
+            const uint32_t scale_row = FP8 ? scales_at(t) : 0;
+            f32x16 acc, part;
+            Frag kf[KD];
+            bf16x8 kx[2], qx[2];
+            f32x4 bs[4];
 #pragma unroll
             for (int k = 0; k < KD; ++k)
                 kf[k] = frag(k);
-            between(-1);
+            between(std::integral_constant<int, -1>{});
+            if constexpr (FP8)
+                kx[0] = bf16_of_codes(kf[0]);
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int k = 0; k < KN; ++k) {
-                if (k == 0)
-                    mfma_first(acc, kf[0], q[0]);
-                else if (k == KN - 1)
-                    mfma_last(acc, kf[k % KD], q[k]);
+            each<KN>([&](auto index) __attribute__((always_inline)) {
+                constexpr int k = index;
+                constexpr int blk = FP8 ? k >> 3 : 0, at = FP8 ? k & 7 : k;
+                constexpr bool end = k == KN - 1 || (FP8 && at == 7);
+                f32x16& sum = blk == 0 ? acc : part;
+                bf16x8 x, y;
+                if constexpr (FP8)
+                    x = kx[k & 1];
                 else
-                    mfma_next(acc, kf[k % KD], q[k]);
-                if (k + KD < KN)
+                    x = kf[k % KD];
+                if constexpr (k < KEPT)
+                    y = q[k];
+                else
+                    y = qx[k % 2];
+                if (at == 0)
+                    mfma_first(sum, x, y);
+                else if (end)
+                    mfma_last(sum, x, y);
+                else
+                    mfma_next(sum, x, y);
+                if constexpr (FP8 && k + 1 < KN)
+                    kx[(k + 1) & 1] = bf16_of_codes(kf[(k + 1) % KD]);
+                if constexpr (!FP8 && k + KD < KN)
                     kf[k % KD] = frag(k + KD);
-                between(k);
+                if constexpr (FP8 && k >= 1 && k - 1 + KD < KN)   // fragment k - 1 + KD takes k - 1's place
+                    kf[(k - 1) % KD] = frag(k - 1 + KD);
+                if constexpr (FP8 && k + 2 >= KEPT && k + 2 < KN)
+                    qx[k % 2] = query(k + 2);
+                if constexpr (FP8) {
+                    if (at == (blk == 4 ? 1 : 4)) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            bs[i] = scales_of(scale_row, blk, i);
+                    }
+                }
+                between(index);
+                if constexpr (FP8 && end) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[i] = blk == 0 ? acc[i] * bs[i >> 2][i & 3] : acc[i] + part[i] * bs[i >> 2][i & 3];
+                }
                 __builtin_amdgcn_sched_barrier(0);
-            }
+            });
             return acc;
         };
         float s[16];        // scores of the tile at hand, in units of log2
@@ -531,7 +722,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             }
         };
         {
-            const f32x16 raw = scores(0, [](int) {});
+            const f32x16 raw = scores(0, [](auto) {});
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 scaled_max(raw, i);
@@ -541,54 +732,101 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 
         for (uint32_t t = 0; t < n_tiles; ++t) {
             enter(t);
-            const char* st = smem + (t & (STAGES - 1)) * STAGE;
-            auto vfrag = [&](int v) __attribute__((always_inline)) {
+            const char* st = smem + stage_of(t);
+            auto vfrag = [&](int v) __attribute__((always_inline)) -> Frag {
                 const int fb = v >> 1, ks = v & 1;
-                const v4i16 lo = lds_tr16(st + v_off[fb & 1][0] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
-                const v4i16 hi = lds_tr16(st + v_off[fb & 1][1] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
-                return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                if constexpr (FP8) {
+                    return lds_tr8(smem + ((stage_of(t) + v_off[0][0]) ^ ((2 * fb & 7) * 16)) + (fb >> 2) * BLOCK_BYTES + ks * 2048);
+                } else {
+                    const v4i16 lo = lds_tr16(st + v_off[fb & 1][0] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
+                    const v4i16 hi = lds_tr16(st + v_off[fb & 1][1] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
+                    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
             };
             const float ref = mref == -INFINITY ? 0.0f : mref;
             // The scores of the next tile, and the weights of this one while the matrix cores
             // run.  (The last step computes scores that nobody uses, from whatever the stage holds.)
             uint32_t pk[8];
             float sum = 0.0f;
-            bf16x8 vf[VD];
+            [[maybe_unused]] float e[16];
+            Frag vf[VD];
             auto weights = [&](int k) __attribute__((always_inline)) {
                 const float e0 = __builtin_amdgcn_exp2f(s[2 * k] - ref);
                 const float e1 = __builtin_amdgcn_exp2f(s[2 * k + 1] - ref);
                 sum += e0 + e1;
-                pk[k] = pack_bf16x2(e0, e1);
+                if constexpr (FP8) {
+                    e[2 * k] = e0;
+                    e[2 * k + 1] = e1;
+                } else {
+                    pk[k] = pack_bf16x2(e0, e1);
+                }
             };
-            const f32x16 raw = scores(t + 1, [&](int k) __attribute__((always_inline)) {
-                if (k < 0) {
+            const f32x16 raw = scores(t + 1, [&](auto index) __attribute__((always_inline)) {
+                constexpr int k = index;
+                if constexpr (k < 0) {
                     weights(0);
                     weights(1);
-                } else if (k % 3 == 0 && k / 3 < 6) {
-                    weights(2 + k / 3);
+                } else if constexpr (FP8 ? k < 6 : k % 3 == 0 && k / 3 < 6) {
+                    weights(2 + (FP8 ? k : k / 3));
                 }
-                if (k >= 0 && k % 4 == 1)
+                if constexpr (k >= 0 && k % 4 == 1 && k / 4 < LOADS)
                     load(k / 4);
-                if (k >= KN - VD)
+                if constexpr (k >= KN - VD)
                     vf[k - (KN - VD)] = vfrag(k - (KN - VD));
             });
             l += sum;
-            const bf16x8 pf[2] = {as_bf16x8(u32x4{pk[0], pk[1], pk[2], pk[3]}),
-                                  as_bf16x8(u32x4{pk[4], pk[5], pk[6], pk[7]})};
+            // e4m3: the weights times the scales of one block of 128 features at a time, rounded
+            // to bf16 once.
+            bf16x8 pf[2];
+            [[maybe_unused]] f32x4 ps[2];
+            auto block_weights = [&](int i) __attribute__((always_inline)) {   // of four rows
+                pk[2 * i] = pack_bf16x2(e[4 * i] * ps[i & 1][0], e[4 * i + 1] * ps[i & 1][1]);
+                pk[2 * i + 1] = pack_bf16x2(e[4 * i + 2] * ps[i & 1][2], e[4 * i + 3] * ps[i & 1][3]);
+            };
+            bf16x8 vx[2];
+            const uint32_t scale_row = FP8 ? scales_at(t) : 0;
+            if constexpr (FP8) {
 #pragma unroll
-            for (int v = 0; v < VN; ++v) {
-                o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[v % VD], pf[v & 1], o[v >> 1], 0, 0, 0);
-                if (v + VD < VN)
-                    vf[v % VD] = vfrag(v + VD);
-                if (v >= 4 && v < 20)
-                    scaled_max(raw, v - 4);
-                if (v == 20)
-                    mx = fmaxf(mx, swap32(mx));
-                if constexpr (PAGE8)
-                    if (v == 24)
-                        next_entry = entry_of(t + 4);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < 4; ++i) {
+                    ps[i & 1] = scales_of(scale_row, 0, i);
+                    block_weights(i);
+                }
+                vx[0] = bf16_of_codes(vf[0]);
             }
+            each<VN>([&](auto index) __attribute__((always_inline)) {
+                constexpr int v = index;
+                if constexpr (v == 0 || (FP8 && (v & 7) == 0)) {
+                    pf[0] = as_bf16x8(u32x4{pk[0], pk[1], pk[2], pk[3]});
+                    pf[1] = as_bf16x8(u32x4{pk[4], pk[5], pk[6], pk[7]});
+                }
+                bf16x8 x;
+                if constexpr (FP8)
+                    x = vx[v & 1];
+                else
+                    x = vf[v % VD];
+                o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pf[v & 1], o[v >> 1], 0, 0, 0);
+                if constexpr (FP8 && v + 1 < VN)
+                    vx[(v + 1) & 1] = bf16_of_codes(vf[(v + 1) % VD]);
+                if constexpr (!FP8 && v + VD < VN)
+                    vf[v % VD] = vfrag(v + VD);
+                if constexpr (FP8 && v >= 1 && v - 1 + VD < VN)
+                    vf[(v - 1) % VD] = vfrag(v - 1 + VD);
+                if constexpr (v >= 4 && v < 20)
+                    scaled_max(raw, v - 4);
+                if constexpr (v == 20)
+                    mx = fmaxf(mx, swap32(mx));
+                if constexpr (PAGE8 && v == 24)
+                    next_entry = entry_of(t + 4);
+                if constexpr (FP8) {
+                    // The next block's weights, a quarter at a time.
+                    constexpr int b = (v >> 3) + 1, at = v & 7;
+                    if constexpr (b < 4 && at >= 3 && at < 7)
+                        block_weights(at - 3);
+                    if constexpr (b < 4 && at >= 1 && at < 5)
+                        ps[(at - 1) & 1] = scales_of(scale_row, b, at - 1);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
             if constexpr (PAGE8)
                 next_id = id_at(next_entry);
             if (t + 1 < n_tiles)
@@ -695,14 +933,15 @@ __global__ void __launch_bounds__(256) tree_attention_join(MfmaParams P)
 
 bool tree_attention_mfma_fits(const TreeAttentionArgs& a, AttnKind kind)
 {
-    return kind == ATTN_BF16 && a.D == D && a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
+    return (kind == ATTN_BF16 || kind == ATTN_E4M3) && a.D == D && a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
+           (kind == ATTN_BF16 || a.Ls.stride_token < (int64_t(1) << 28)) &&
            (uint64_t)a.L.batch * a.L.max_pages < (uint64_t(1) << 32) &&
            // items (at most one partly filled per request) times tiles
            ((uint64_t)a.T * a.H / kAttnRows + std::min<uint64_t>(a.L.batch, a.T)) * (a.capacity / TILE + 1) <
                (uint64_t(1) << 31);
 }
 
-hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, hipStream_t s)
+hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind, hipStream_t s)
 {
     MfmaParams P{};
     P.a = a;
@@ -719,11 +958,12 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, hipStream_t s)
     const int64_t waves = (std::min<int64_t>((int64_t)a.T * a.H, kAttnRows) + 31) / 32;
     P.piece = (uint32_t)(waves * PIECE_WAVE);
     P.min_tiles = 4;
-    log_launch("tree_attention_mfma", kAttnGroups, 64 * WAVES, "T=%d H=%d page_size=%u", a.T, a.H, ps);
-    if (ps % 8 == 0)
-        hipLaunchKernelGGL(tree_attention_mfma<true>, dim3(kAttnGroups), dim3(64 * WAVES), 0, s, P);
-    else
-        hipLaunchKernelGGL(tree_attention_mfma<false>, dim3(kAttnGroups), dim3(64 * WAVES), 0, s, P);
+    const bool fp8 = kind == ATTN_E4M3;
+    log_launch(fp8 ? "tree_attention_mfma<e4m3>" : "tree_attention_mfma<bf16>", kAttnGroups, 64 * WAVES,
+               "T=%d H=%d page_size=%u", a.T, a.H, ps);
+    auto* kernel = fp8 ? (ps % 8 == 0 ? tree_attention_mfma<true, true> : tree_attention_mfma<false, true>)
+                       : (ps % 8 == 0 ? tree_attention_mfma<true, false> : tree_attention_mfma<false, false>);
+    hipLaunchKernelGGL(kernel, dim3(kAttnGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
     log_launch("tree_attention_join", (kAttnGroups - 1) * 4, 256, "T=%d H=%d", a.T, a.H);
