@@ -228,7 +228,7 @@ MLA_API size_t mla_tree_attention_workspace_size(int32_t total_tokens, int32_t n
         return 0;
     // Two partial results per workgroup: whole waves of 32 rows of K sums, a maximum and a sum each.
     const int64_t rows = (std::min<int64_t>((int64_t)total_tokens * num_heads, kAttnRows) + 31) / 32 * 32;
-    return align256((size_t)(2 * kAttnGroups * rows * (K + 2)) * sizeof(float));
+    return align256((size_t)(2 * kAttnGroups * rows * (K + 2)) * sizeof(float) + kAttnGroups * kAttnCutBytes);
 }
 
 namespace {

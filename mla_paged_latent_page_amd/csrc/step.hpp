@@ -50,6 +50,7 @@ struct TreeAttentionArgs {
 // (the item its share begins in and the one it ends in).
 constexpr int kAttnGroups = 256;      // workgroups, one per CU: the whole LDS and register file
 constexpr int kAttnRows = 128;        // query rows (tokens x heads) of an item
+constexpr int kAttnCutBytes = 32;     // and a record of the cut it starts at
 
 enum AttnKind { ATTN_F32, ATTN_BF16, ATTN_E4M3 };
 

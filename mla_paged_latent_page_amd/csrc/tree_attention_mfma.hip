@@ -46,10 +46,19 @@ __device__ __attribute__((always_inline)) inline void each(F&& f)
     each(f, std::make_integer_sequence<int, N>{});
 }
 
+// What the join needs of the cut a workgroup starts at; every workgroup leaves one.
+struct Cut {
+    uint32_t w, w0, w1;                      // this cut, and the first and last one inside its item
+    uint32_t row0, rows;                     // first query row of the item, rows it has (0: no split item)
+    uint32_t pad[3];
+};
+static_assert(sizeof(Cut) == kAttnCutBytes, "workspace");
+
 struct MfmaParams {
     TreeAttentionArgs a;
     uint32_t ps_magic, ps_shift;             // p / page_size = mulhi(p, magic) >> shift for p < 2^31
     uint32_t piece;                          // floats of a partial result slot
+    Cut* cuts;                               // [kAttnGroups]
     int min_tiles;                           // least tiles of a workgroup's share
 };
 
@@ -250,17 +259,29 @@ __device__ inline void wait_loads()
 // instruction, so each waits two states for operands just written by vector instructions, and
 // the last one of a chain for its result before anything can read it (12 wait states after 8
 // passes; back-to-back products into the same registers need none).
+template <bool FRESH>   // operands just written by vector instructions
 __device__ inline void mfma_first(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
+    if constexpr (FRESH)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
+    else
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
 }
+template <bool FRESH>
 __device__ inline void mfma_next(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
+    if constexpr (FRESH)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
+    else
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
 }
+template <bool FRESH>
 __device__ inline void mfma_last(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
+    if constexpr (FRESH)
+        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
+    else
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
 }
 
 // Element e of an output sum times f, in its accumulation register (written out, as the
@@ -323,13 +344,25 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
     // then read the same rows through one L2.
     const uint32_t per = (sched.groups + 7) / 8;
     const uint32_t w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((blockIdx.x >> 3) >= per || w >= sched.groups || sched.total == 0)
+    const bool idle = (blockIdx.x >> 3) >= per || w >= sched.groups || sched.total == 0;
+    Request r{};
+    uint32_t stop = sched.total, u = 0;
+    Cut rec{};
+    if (!idle) {
+        if (w + 1 < sched.groups)
+            stop = uniform(sched.cut(w + 1, r));
+        u = uniform(sched.cut(w, r));
+        if (u == sched.raw(w)) {
+            const uint32_t m = (u - r.base) / r.nt, lo = r.base + m * r.nt;
+            if (u != lo)   // (an end of an item may be a cut, within `snap` of it)
+                rec = Cut{w, sched.first_cut_past(lo + sched.snap), sched.first_cut_past(lo + r.nt - sched.snap - 1) - 1,
+                          r.t0 * (uint32_t)a.H + m * kAttnRows, r.n * (uint32_t)a.H - m * kAttnRows, {}};
+        }
+    }
+    if (threadIdx.x == 0)
+        P.cuts[blockIdx.x] = rec;
+    if (idle)
         return;
-    Request r;
-    uint32_t stop = sched.total;
-    if (w + 1 < sched.groups)
-        stop = uniform(sched.cut(w + 1, r));
-    uint32_t u = uniform(sched.cut(w, r));
 
     // Lane-constant offsets.  A tile is stored in blocks of 32 rows x 128 bytes (64 bf16 columns
     // or 128 codes); the 16-byte granule g of row x sits at g ^ f(x), f(x) a permutation of bits
@@ -349,15 +382,20 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         k_off[s] = FP8 ? (s == 0 ? col * 128 + fk * 16 : col * 64 + (col >> 2 & 3) * 16) + half * 8 : col * 128 + (((2 * s + half) ^ fk) * 16);
     // Transposing reads.  bf16: lane c of a 16-lane group addresses row c / 4 and 8 bytes of its
     // columns; e4m3: row c / 2 of the eight (rows 0 .. 3 and 8 .. 11, + 4 half) and 8 codes.
-    const uint32_t c16 = lane & 15, vrow = 4 * half + (FP8 ? (c16 >> 1 & 3) + 8 * (c16 >> 3) : c16 >> 2);
-    uint32_t v_off[2][2];   // bf16: [feature block parity][rows vrow or vrow + 8]; e4m3: [0][0]
+    [[maybe_unused]] uint32_t v_off[2][2];   // bf16: [feature block parity][rows vrow or vrow + 8]
+    if constexpr (!FP8) {
+        const uint32_t c16 = lane & 15, vrow = 4 * half + (c16 >> 2);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            v_off[s][h] = FP8 ? vrow * 128 + (c16 & 1) * 8 + (((uint32_t)(lane >> 4 & 1) ^ f(vrow)) * 16)
-                              : (vrow + 8 * h) * 128 + (c16 & 1) * 8 +
-                                    (((uint32_t)(4 * s + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ f(vrow + 8 * h)) * 16);
+            for (int h = 0; h < 2; ++h)
+                v_off[s][h] = (vrow + 8 * h) * 128 + (c16 & 1) * 8 +
+                              (((uint32_t)(4 * s + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ f(vrow + 8 * h)) * 16);
+    }
+    auto v_off8 = [&]() __attribute__((always_inline)) {
+        const uint32_t ln = lane_again(), c16 = ln & 15, vrow = 4 * (ln >> 5) + (c16 >> 1 & 3) + 8 * (c16 >> 3);
+        return vrow * 128 + (c16 & 1) * 8 + (((ln >> 4 & 1) ^ f(vrow)) * 16);
+    };
     const uint32_t lds0 = lds_addr(smem);
     // Stage of tile t (the tiles of an item counted from 0).
     auto stage_of = [](uint32_t t) __attribute__((always_inline)) { return (t & (STAGES - 1)) * (FP8 ? STAGE8 : STAGE); };
@@ -616,7 +654,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 
         // Scores of tile t: lane (col, half) gets rows 8 (i / 4) + 4 half + i % 4 for its query.
         // Fragments are read KD products ahead; `between(k)` is other work during product k.
-        // e4m3: codes become bf16 on the way to the matrix cores, one product ahead; each block
+        // e4m3: codes become bf16 on the way to the matrix cores; each block
         // of 128 columns has sums of its own, times the block's scale of each row.
         constexpr int KN = D / 16, KD = FP8 ? 5 : 6, VN = 2 * (K / 32), VD = 4;
         using Frag = std::conditional_t<FP8, u32x2, bf16x8>;
@@ -635,41 +673,33 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             const uint32_t scale_row = FP8 ? scales_at(t) : 0;
             f32x16 acc, part;
             Frag kf[KD];
-            bf16x8 kx[2], qx[2];
+            bf16x8 qx[2];
             f32x4 bs[4];
 #pragma unroll
             for (int k = 0; k < KD; ++k)
                 kf[k] = frag(k);
             between(std::integral_constant<int, -1>{});
-            if constexpr (FP8)
-                kx[0] = bf16_of_codes(kf[0]);
             __builtin_amdgcn_sched_barrier(0);
             each<KN>([&](auto index) __attribute__((always_inline)) {
                 constexpr int k = index;
                 constexpr int blk = FP8 ? k >> 3 : 0, at = FP8 ? k & 7 : k;
                 constexpr bool end = k == KN - 1 || (FP8 && at == 7);
                 f32x16& sum = blk == 0 ? acc : part;
-                bf16x8 x, y;
-                if constexpr (FP8)
-                    x = kx[k & 1];
-                else
-                    x = kf[k % KD];
+                // (the conversion runs in the shadow of the product before)
+                const bf16x8 x = bf16_of_codes(kf[k % KD]);
+                bf16x8 y;
                 if constexpr (k < KEPT)
                     y = q[k];
                 else
                     y = qx[k % 2];
                 if (at == 0)
-                    mfma_first(sum, x, y);
+                    mfma_first<FP8>(sum, x, y);
                 else if (end)
-                    mfma_last(sum, x, y);
+                    mfma_last<FP8>(sum, x, y);
                 else
-                    mfma_next(sum, x, y);
-                if constexpr (FP8 && k + 1 < KN)
-                    kx[(k + 1) & 1] = bf16_of_codes(kf[(k + 1) % KD]);
-                if constexpr (!FP8 && k + KD < KN)
+                    mfma_next<FP8>(sum, x, y);
+                if constexpr (k + KD < KN)
                     kf[k % KD] = frag(k + KD);
-                if constexpr (FP8 && k >= 1 && k - 1 + KD < KN)   // fragment k - 1 + KD takes k - 1's place
-                    kf[(k - 1) % KD] = frag(k - 1 + KD);
                 if constexpr (FP8 && k + 2 >= KEPT && k + 2 < KN)
                     qx[k % 2] = query(k + 2);
                 if constexpr (FP8) {
@@ -733,10 +763,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         for (uint32_t t = 0; t < n_tiles; ++t) {
             enter(t);
             const char* st = smem + stage_of(t);
+            const uint32_t v_at = FP8 ? stage_of(t) + v_off8() : 0;
             auto vfrag = [&](int v) __attribute__((always_inline)) -> Frag {
                 const int fb = v >> 1, ks = v & 1;
                 if constexpr (FP8) {
-                    return lds_tr8(smem + ((stage_of(t) + v_off[0][0]) ^ ((2 * fb & 7) * 16)) + (fb >> 2) * BLOCK_BYTES + ks * 2048);
+                    return lds_tr8(smem + (v_at ^ ((2 * fb & 7) * 16)) + (fb >> 2) * BLOCK_BYTES + ks * 2048);
                 } else {
                     const v4i16 lo = lds_tr16(st + v_off[fb & 1][0] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
                     const v4i16 hi = lds_tr16(st + v_off[fb & 1][1] + (fb >> 1) * BLOCK_BYTES + ks * 2048);
@@ -783,7 +814,6 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 pk[2 * i] = pack_bf16x2(e[4 * i] * ps[i & 1][0], e[4 * i + 1] * ps[i & 1][1]);
                 pk[2 * i + 1] = pack_bf16x2(e[4 * i + 2] * ps[i & 1][2], e[4 * i + 3] * ps[i & 1][3]);
             };
-            bf16x8 vx[2];
             const uint32_t scale_row = FP8 ? scales_at(t) : 0;
             if constexpr (FP8) {
 #pragma unroll
@@ -791,7 +821,6 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     ps[i & 1] = scales_of(scale_row, 0, i);
                     block_weights(i);
                 }
-                vx[0] = bf16_of_codes(vf[0]);
             }
             each<VN>([&](auto index) __attribute__((always_inline)) {
                 constexpr int v = index;
@@ -799,18 +828,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     pf[0] = as_bf16x8(u32x4{pk[0], pk[1], pk[2], pk[3]});
                     pf[1] = as_bf16x8(u32x4{pk[4], pk[5], pk[6], pk[7]});
                 }
-                bf16x8 x;
-                if constexpr (FP8)
-                    x = vx[v & 1];
-                else
-                    x = vf[v % VD];
-                o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pf[v & 1], o[v >> 1], 0, 0, 0);
-                if constexpr (FP8 && v + 1 < VN)
-                    vx[(v + 1) & 1] = bf16_of_codes(vf[(v + 1) % VD]);
-                if constexpr (!FP8 && v + VD < VN)
+                o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of_codes(vf[v % VD]), pf[v & 1], o[v >> 1], 0, 0, 0);
+                if constexpr (v + VD < VN)
                     vf[v % VD] = vfrag(v + VD);
-                if constexpr (FP8 && v >= 1 && v - 1 + VD < VN)
-                    vf[(v - 1) % VD] = vfrag(v - 1 + VD);
                 if constexpr (v >= 4 && v < 20)
                     scaled_max(raw, v - 4);
                 if constexpr (v == 20)
@@ -858,74 +878,175 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
     }
 }
 
-// Joins the pieces of split items.  Block (w, g): if cut w lies inside an item, rows 32 g ..
-// of that item; the blocks of all cuts inside one item share its 64 column groups (quads of
-// features in the lane order of the accumulators).
+// Joins the pieces of split items.  Block (i, g): rows 32 g .. of the item that cut record i
+// lies in, if any; the blocks of all cuts inside one item share its 64 quads of features (in
+// the lane order of the accumulators).  With many pieces the waves of a block share the pieces,
+// else the quads: pieces of two shares each are read by 4 waves at once either way.
 __global__ void __launch_bounds__(256) tree_attention_join(MfmaParams P)
 {
+    __shared__ float factor[kAttnGroups][32];    // per piece and row: its maximum, then its weight
+    __shared__ float top[8][32];
+    __shared__ f32x4 part[3][2][64];
     const TreeAttentionArgs& a = P.a;
+    const uint32_t g = blockIdx.x & 3;
+    const auto* words = (const __attribute__((address_space(4))) uint32_t*)(uint64_t)(P.cuts + (blockIdx.x >> 2));
+    const Cut rec{words[0], words[1], words[2], words[3], words[4], {}};
+    if (rec.rows <= g * 32)
+        return;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, col = lane & 31;
-    const uint32_t w = 1 + (blockIdx.x >> 2), g = blockIdx.x & 3;
-    Schedule sched(a, lane, P.min_tiles);
-    if (w >= sched.groups || sched.total == 0)
-        return;
-    Request r;
-    const uint32_t cut = sched.cut(w, r);
-    if (cut != sched.raw(w))
-        return;
-    const uint32_t m = (cut - r.base) / r.nt;
-    const uint32_t lo = r.base + m * r.nt, hi = lo + r.nt;
-    if (cut == lo)
-        return;
-    const uint32_t rows = r.n * (uint32_t)a.H;
-    const uint32_t row = m * kAttnRows + g * 32 + col;
-    if (m * kAttnRows + g * 32 >= rows)
-        return;
-    // First and last cut inside the item (an end of an item may be a cut, within `snap` of it).
-    const uint32_t w0 = sched.first_cut_past(lo + sched.snap);
-    const uint32_t w1 = sched.first_cut_past(hi - sched.snap - 1) - 1;
-    const uint32_t pieces = w1 - w0 + 2;
+    const uint32_t w0 = rec.w0, w1 = rec.w1;
+    const bool valid = g * 32 + col < rec.rows;
+    const int64_t qrow = rec.row0 + g * 32 + (valid ? col : 0);
+    const uint32_t share = rec.w - w0, shares = w1 - w0 + 1;
+    const uint32_t pieces = shares + 1;          // at most kAttnGroups
     // Piece 0 is the end of share w0 - 1, piece k the start of share w0 + k - 1.
+    const float* first = a.ws + (size_t)(2 * (w0 - 1) + 1) * P.piece + (size_t)g * PIECE_WAVE;
+    const float* rest = a.ws + (size_t)(2 * w0) * P.piece + (size_t)g * PIECE_WAVE;
     auto piece = [&](uint32_t k) __attribute__((always_inline)) {
-        const uint32_t slot = k == 0 ? 2 * (w0 - 1) + 1 : 2 * (w0 + k - 1);
-        return a.ws + (size_t)slot * P.piece + (size_t)g * PIECE_WAVE;
+        return k == 0 ? first : rest + (size_t)(k - 1) * 2 * P.piece;
     };
-    float mx = -INFINITY;
-    for (uint32_t k = 0; k < pieces; ++k)
-        mx = fmaxf(mx, piece(k)[32 * K + col]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f;
-    for (uint32_t k = 0; k < pieces; ++k)
-        l += piece(k)[32 * K + 32 + col] * __builtin_amdgcn_exp2f(piece(k)[32 * K + col] - ref);
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    const uint32_t qrow = r.t0 * (uint32_t)a.H + min(row, rows - 1);
-    const uint32_t share = (w - w0) * 4 + wave, shares = (w1 - w0 + 1) * 4;
-    if (a.lse && share == 0 && half == 0 && row < rows)
-        a.lse[qrow] = l == 0.0f ? -INFINITY : mx * kLn2 + __logf(l);
-    for (uint32_t quad = share; quad < 64; quad += shares) {
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        constexpr int U = 8;
-        for (uint32_t k0 = 0; k0 < pieces; k0 += U) {
-            f32x4 v[U];
-            float f[U];
+    auto finish = [&](uint32_t quad, f32x4 v) __attribute__((always_inline)) {
+        if (valid && quad < 64)
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + qrow * K + (quad >> 2) * 32 + (quad & 3) * 8 +
+                                      half * 4) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    };
+    auto finish_lse = [&](float mx, float l) __attribute__((always_inline)) {
+        if (a.lse && share == 0 && threadIdx.x < 32 && valid)
+            a.lse[qrow] = l == 0.0f ? -INFINITY : mx * kLn2 + __logf(l);
+    };
+
+    constexpr uint32_t FEW = 8;
+    if (pieces <= FEW) {
+        float f[FEW], s[FEW];
+        float mx = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const float* p = piece(min(k0 + i, pieces - 1));
-                v[i] = *reinterpret_cast<const f32x4*>(p + (quad * 64 + lane) * 4);
-                f[i] = p[32 * K + col];
+        for (uint32_t k = 0; k < FEW; ++k) {
+            const float* src = piece(min(k, pieces - 1)) + 32 * K + col;
+            f[k] = k < pieces ? src[0] : -INFINITY;
+            s[k] = src[32];
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < FEW; ++k)
+            mx = fmaxf(mx, f[k]);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        float l = 0.0f;
+#pragma unroll
+        for (uint32_t k = 0; k < FEW; ++k) {
+            f[k] = k < pieces ? __builtin_amdgcn_exp2f(f[k] - ref) : 0.0f;
+            l += k < pieces ? s[k] * f[k] : 0.0f;
+        }
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        finish_lse(mx, l);
+        constexpr int Q = 4;
+        const uint32_t step = shares * WAVES;
+        for (uint32_t q0 = share * WAVES + wave; q0 < 64; q0 += step * Q) {
+            f32x4 sum[Q];
+#pragma unroll
+            for (int j = 0; j < Q; ++j)
+                sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (uint32_t k = 0; k < FEW; k += 2) {
+                if (k < pieces) {
+                    f32x4 v[2][Q];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < Q; ++j)
+                            v[i][j] = *reinterpret_cast<const f32x4*>(piece(min(k + i, pieces - 1)) +
+                                                                      (min(q0 + step * j, 63u) * 64 + lane) * 4);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (k + i < pieces)
+#pragma unroll
+                            for (int j = 0; j < Q; ++j)
+                                sum[j] += v[i][j] * f[k + i];
+                }
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                if (k0 + i < pieces)
-                    sum += v[i] * __builtin_amdgcn_exp2f(f[i] - ref);
+            for (int j = 0; j < Q; ++j)
+                finish(q0 + step * j, sum[j] * inv);
         }
-        sum *= inv;
-        if (row < rows)
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (int64_t)qrow * K + (quad >> 2) * 32 +
-                                      (quad & 3) * 8 + half * 4) =
-                u32x2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+        return;
+    }
+
+    // Weights of the pieces: thread (p, x) takes row x of pieces p, p + 8, ...
+    const uint32_t p = threadIdx.x >> 5, x = threadIdx.x & 31;
+    float mx = -INFINITY;
+    for (uint32_t k0 = p; k0 < pieces; k0 += 32) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = piece(min(k0 + 8 * i, pieces - 1))[32 * K + x];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k0 + 8 * i < pieces) {
+                factor[k0 + 8 * i][x] = v[i];
+                mx = fmaxf(mx, v[i]);
+            }
+    }
+    top[p][x] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        mx = fmaxf(mx, top[i][x]);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float l = 0.0f;
+    for (uint32_t k0 = p; k0 < pieces; k0 += 32) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = piece(min(k0 + 8 * i, pieces - 1))[32 * K + 32 + x];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k0 + 8 * i < pieces) {
+                const float f = __builtin_amdgcn_exp2f(factor[k0 + 8 * i][x] - ref);
+                factor[k0 + 8 * i][x] = f;
+                l += v[i] * f;
+            }
+    }
+    __syncthreads();
+    top[p][x] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        l += top[i][col];
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    finish_lse(mx, l);   // thread x < 32 holds row x of both
+
+    // Quads share, share + shares, ...: two at a time, the wave's pieces four at a time.
+    constexpr int Q = 2, U = 4;
+    for (uint32_t q0 = share; q0 < 64; q0 += shares * Q) {
+        f32x4 sum[Q] = {};
+        for (uint32_t k0 = wave; k0 < pieces; k0 += WAVES * U) {
+            f32x4 v[U][Q];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int j = 0; j < Q; ++j)
+                    v[i][j] = *reinterpret_cast<const f32x4*>(piece(min(k0 + WAVES * i, pieces - 1)) +
+                                                              (min(q0 + shares * j, 63u) * 64 + lane) * 4);
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (k0 + WAVES * i < pieces) {
+                    const float f = factor[k0 + WAVES * i][col];
+#pragma unroll
+                    for (int j = 0; j < Q; ++j)
+                        sum[j] += v[i][j] * f;
+                }
+        }
+        if (wave > 0)
+#pragma unroll
+            for (int j = 0; j < Q; ++j)
+                part[wave - 1][j][lane] = sum[j];
+        __syncthreads();
+        if (wave == 0)
+#pragma unroll
+            for (int j = 0; j < Q; ++j)
+                finish(q0 + shares * j, ((sum[j] + part[0][j][lane]) + (part[1][j][lane] + part[2][j][lane])) * inv);
+        __syncthreads();
     }
 }
 
@@ -958,6 +1079,7 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind,
     const int64_t waves = (std::min<int64_t>((int64_t)a.T * a.H, kAttnRows) + 31) / 32;
     P.piece = (uint32_t)(waves * PIECE_WAVE);
     P.min_tiles = 4;
+    P.cuts = reinterpret_cast<Cut*>(a.ws + (size_t)2 * kAttnGroups * P.piece);
     const bool fp8 = kind == ATTN_E4M3;
     log_launch(fp8 ? "tree_attention_mfma<e4m3>" : "tree_attention_mfma<bf16>", kAttnGroups, 64 * WAVES,
                "T=%d H=%d page_size=%u", a.T, a.H, ps);
@@ -966,8 +1088,10 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind,
     hipLaunchKernelGGL(kernel, dim3(kAttnGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
-    log_launch("tree_attention_join", (kAttnGroups - 1) * 4, 256, "T=%d H=%d", a.T, a.H);
-    hipLaunchKernelGGL(tree_attention_join, dim3((kAttnGroups - 1) * 4), dim3(256), 0, s, P);
+    // One block per cut and 32 rows of an item.
+    const unsigned join_blocks = kAttnGroups * 4;
+    log_launch("tree_attention_join", join_blocks, 256, "T=%d H=%d", a.T, a.H);
+    hipLaunchKernelGGL(tree_attention_join, dim3(join_blocks), dim3(256), 0, s, P);
     return hipGetLastError();
 }
 
