@@ -69,11 +69,13 @@ __device__ inline uint64_t uniform(uint64_t v)
 }
 __device__ inline uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
-// Rows of a request and its share of the work: nm items of 128 query rows, nt tiles each.
+// Rows of a request and its share of the work: nm items of 128 query rows.  An item counts as
+// ITEM_COST units before its tiles' one each: fetching its queries, filling the ring and
+// writing its results takes about as long as that many tiles.
+constexpr uint32_t ITEM_COST = 8;
 struct Request {
-    uint32_t b, t0, n, cached, len, nm, nt;
-    uint32_t base;                           // tiles of all requests before it
-    uint32_t items;                          // items of all requests before it
+    uint32_t b, t0, n, cached, len, nm, nu;  // nu = ITEM_COST + tiles
+    uint32_t base;                           // units of all requests before it
 };
 
 __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
@@ -87,7 +89,7 @@ __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
     r.cached = min(a.cache_len[b], a.capacity);
     r.len = min(r.cached + r.n, a.capacity);
     r.nm = (r.n * (uint32_t)a.H + kAttnRows - 1) / kAttnRows;   // n * H below 2^31 / D
-    r.nt = (r.len + TILE - 1) / TILE;
+    r.nu = (r.len + TILE - 1) / TILE + ITEM_COST;
     return r;
 }
 
@@ -95,7 +97,7 @@ __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
 __device__ inline Request uniform(Request r)
 {
     return Request{uniform(r.b), uniform(r.t0), uniform(r.n), uniform(r.cached), uniform(r.len), uniform(r.nm),
-                   uniform(r.nt), uniform(r.base)};
+                   uniform(r.nu), uniform(r.base)};
 }
 
 __device__ inline uint32_t wave_inclusive(uint32_t v, int lane)
@@ -108,18 +110,18 @@ __device__ inline uint32_t wave_inclusive(uint32_t v, int lane)
     return v;
 }
 
-// The schedule: all tiles (of all items of all requests, in that order) in equal shares.
-// A cut that falls within `snap` tiles of an item's end is moved there: the item is then
-// not split for so little.  Every wave works it out for itself; the requests of the last 64
-// looked at stay in its lanes.  The host has checked that the tiles number below 2^31.
+// The schedule: all units (of all items of all requests, in that order) in equal shares.  A
+// cut that falls within `snap` tiles of an item's first or last one is moved there: the item
+// is then not split for so little.  Every wave works it out for itself; the requests of the last 64
+// looked at stay in its lanes.  The host has checked that the units number below 2^31.
 struct Schedule {
     const TreeAttentionArgs& a;
     int lane;
     uint32_t total, groups, share, rest, snap;
     uint32_t first;                          // first request in the lanes
-    uint32_t before;                         // tiles before it
+    uint32_t before;                         // units before it
     Request mine;
-    uint32_t scan;                           // tiles up to and including mine, from `before`
+    uint32_t scan;                           // units up to and including mine, from `before`
 
     __device__ void load(uint32_t b0, uint32_t tiles_before)
     {
@@ -128,7 +130,7 @@ struct Schedule {
         mine = Request{};
         if (b0 + lane < a.L.batch)
             mine = request_at(a, b0 + lane);
-        scan = wave_inclusive(mine.nm * mine.nt, lane);
+        scan = wave_inclusive(mine.nm * mine.nu, lane);
     }
     __device__ uint32_t loaded() const { return (uint32_t)__builtin_amdgcn_readlane((int)scan, 63); }
 
@@ -170,8 +172,8 @@ struct Schedule {
         r.cached = get(mine.cached);
         r.len = get(mine.len);
         r.nm = get(mine.nm);
-        r.nt = get(mine.nt);
-        r.base = uniform(before + get(scan) - r.nm * r.nt);
+        r.nu = get(mine.nu);
+        r.base = uniform(before + get(scan) - r.nm * r.nu);
         return r;
     }
     // Cut w, and the request it lies in.
@@ -179,8 +181,8 @@ struct Schedule {
     {
         const uint32_t x = raw(w);
         r = find(x);
-        const uint32_t lo = r.base + (x - r.base) / r.nt * r.nt;
-        return x - lo <= snap ? lo : lo + r.nt - x <= snap ? lo + r.nt : x;
+        const uint32_t lo = r.base + (x - r.base) / r.nu * r.nu;
+        return x - lo <= ITEM_COST + snap ? lo : lo + r.nu - x <= snap ? lo + r.nu : x;
     }
 };
 
@@ -204,24 +206,55 @@ __device__ inline float swap32(float v)
     return __builtin_bit_cast(float, (threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-// 16 (or 4) bytes per lane into LDS at lds + 16 (4) * lane, by the lanes of the masks lo and
-// hi: from a uniform base and a 32-bit lane offset, or from a lane address.
+// N loads of 16 bytes per lane into LDS, load j from 128 j bytes past the lane's address to
+// lds + j * BLOCK_BYTES + 16 * lane (the instruction's offset moves both), by the lanes of the
+// masks lo and hi; from a uniform base and a 32-bit lane offset, or from a lane address.  One
+// piece of assembly, as the masks are the whole wave's.
+#define MLA_LOAD(addr, offset) "global_load_lds_dwordx4 " addr " offset:" offset "\n\t"
+#define MLA_NEXT "s_add_u32 m0, m0, 3968\n\t"
+#define MLA_LOADS(N, addr)                                                                                        \
+    if constexpr (J == 0 && N == 3)                                                                               \
+        asm volatile(MLA_ON MLA_LOAD(addr, "0") MLA_NEXT MLA_LOAD(addr, "128") MLA_NEXT MLA_LOAD(addr, "256")     \
+                     MLA_OFF MLA_ARGS);                                                                           \
+    else if constexpr (J == 3 && N == 3)                                                                          \
+        asm volatile(MLA_ON MLA_LOAD(addr, "384") MLA_NEXT MLA_LOAD(addr, "512") MLA_NEXT MLA_LOAD(addr, "640")   \
+                     MLA_OFF MLA_ARGS);                                                                           \
+    else if constexpr (J == 6 && N == 3)                                                                          \
+        asm volatile(MLA_ON MLA_LOAD(addr, "768") MLA_NEXT MLA_LOAD(addr, "896") MLA_NEXT MLA_LOAD(addr, "1024")  \
+                     MLA_OFF MLA_ARGS);                                                                           \
+    else if constexpr (J == 0 && N == 2)                                                                          \
+        asm volatile(MLA_ON MLA_LOAD(addr, "0") MLA_NEXT MLA_LOAD(addr, "128") MLA_OFF MLA_ARGS);                 \
+    else if constexpr (J == 2 && N == 2)                                                                          \
+        asm volatile(MLA_ON MLA_LOAD(addr, "256") MLA_NEXT MLA_LOAD(addr, "384") MLA_OFF MLA_ARGS);               \
+    else                                                                                                          \
+        asm volatile(MLA_ON MLA_LOAD(addr, "0") MLA_OFF MLA_ARGS)
+#define MLA_ON "s_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %0\n\t"
+#define MLA_OFF "s_mov_b64 exec, -1"
+
+template <int J, int N>
 __device__ inline void load_lds(const char* base, uint32_t voff, uint32_t lds, uint32_t lo, uint32_t hi)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\t"
-                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
-                 :
-                 : "s"(lds), "v"(voff), "s"(base), "s"(lo), "s"(hi)
-                 : "memory", "m0");
+    lds += J * (BLOCK_BYTES - 128);
+#define MLA_ARGS : : "s"(lds), "v"(voff), "s"(lo), "s"(hi), "s"(base) : "memory", "m0", "scc"
+    MLA_LOADS(N, "%1, %4");
+#undef MLA_ARGS
 }
+template <int J, int N>
 __device__ inline void load_lds(const char* src, uint32_t lds, uint32_t lo, uint32_t hi)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\t"
-                 "global_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1"
-                 :
-                 : "s"(lds), "v"(src), "s"(lo), "s"(hi)
-                 : "memory", "m0");
+    lds += J * (BLOCK_BYTES - 128);
+#define MLA_ARGS : : "s"(lds), "v"(src), "s"(lo), "s"(hi) : "memory", "m0", "scc"
+    MLA_LOADS(N, "%1, off");
+#undef MLA_ARGS
 }
+#undef MLA_OFF
+#undef MLA_ON
+#undef MLA_LOADS
+#undef MLA_NEXT
+#undef MLA_LOAD
+static_assert(BLOCK_BYTES - 128 == 3968, "the step of m0 in the loads");
+
+// 4 bytes per lane.
 __device__ inline void load_lds4(const char* base, uint32_t voff, uint32_t lds, uint32_t lo, uint32_t hi)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %4\n\t"
@@ -256,9 +289,10 @@ __device__ inline void wait_loads()
 
 // One product with its sums in ordinary registers: the output sums take all 256 accumulation
 // registers, and the compiler would put these there too.  It does not see that this is a matrix
-// instruction, so each waits two states for operands just written by vector instructions, and
-// the last one of a chain for its result before anything can read it (12 wait states after 8
-// passes; back-to-back products into the same registers need none).
+// instruction, so each one waits two states for operands just written by vector instructions,
+// and the last one of a chain for its result before anything can read it (12 wait states after
+// 8 passes; back-to-back products into the same registers need none).  Nor must it move the
+// sums inside a chain: tests/test_matrix_waits.py reads the generated code for that.
 template <bool FRESH>   // operands just written by vector instructions
 __device__ inline void mfma_first(f32x16& acc, bf16x8 x, bf16x8 y)
 {
@@ -275,13 +309,18 @@ __device__ inline void mfma_next(f32x16& acc, bf16x8 x, bf16x8 y)
     else
         asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
 }
+// FRESH: into the same registers; else into others, where the result stays.
 template <bool FRESH>
-__device__ inline void mfma_last(f32x16& acc, bf16x8 x, bf16x8 y)
+__device__ inline f32x16 mfma_last(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    if constexpr (FRESH)
+    if constexpr (FRESH) {
         asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
-    else
-        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
+        return acc;
+    } else {
+        f32x16 out;
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %3\n\ts_nop 13" : "=&v"(out) : "v"(x), "v"(y), "v"(acc));
+        return out;
+    }
 }
 
 // Element e of an output sum times f, in its accumulation register (written out, as the
@@ -353,9 +392,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             stop = uniform(sched.cut(w + 1, r));
         u = uniform(sched.cut(w, r));
         if (u == sched.raw(w)) {
-            const uint32_t m = (u - r.base) / r.nt, lo = r.base + m * r.nt;
+            const uint32_t m = (u - r.base) / r.nu, lo = r.base + m * r.nu;
             if (u != lo)   // (an end of an item may be a cut, within `snap` of it)
-                rec = Cut{w, sched.first_cut_past(lo + sched.snap), sched.first_cut_past(lo + r.nt - sched.snap - 1) - 1,
+                rec = Cut{w, sched.first_cut_past(lo + ITEM_COST + sched.snap),
+                          sched.first_cut_past(lo + r.nu - sched.snap - 1) - 1,
                           r.t0 * (uint32_t)a.H + m * kAttnRows, r.n * (uint32_t)a.H - m * kAttnRows, {}};
         }
     }
@@ -399,20 +439,21 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
     const uint32_t lds0 = lds_addr(smem);
     // Stage of tile t (the tiles of an item counted from 0).
     auto stage_of = [](uint32_t t) __attribute__((always_inline)) { return (t & (STAGES - 1)) * (FP8 ? STAGE8 : STAGE); };
-    const float c = a.scale * kLog2e;
+    const float c = fabsf(a.scale) * kLog2e;   // a negative scale turns the queries' signs; 0 is not taken
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 
     while (u < stop) {
-        while (u >= r.base + r.nm * r.nt) {
-            const uint32_t next = r.base + r.nm * r.nt;
+        while (u >= r.base + r.nm * r.nu) {
+            const uint32_t next = r.base + r.nm * r.nu;
             r = request_at(a, r.b + 1);
             r.base = next;
             r = uniform(r);
         }
-        const uint32_t m = uniform((u - r.base) / r.nt);
-        const uint32_t item = r.base + m * r.nt;
-        const uint32_t tile0 = u - item;
-        const uint32_t tile1 = min(stop, item + r.nt) - item;
-        u = item + tile1;
+        const uint32_t m = uniform((u - r.base) / r.nu);
+        const uint32_t item = r.base + m * r.nu;
+        const uint32_t tile0 = u - item < ITEM_COST ? 0 : u - item - ITEM_COST;
+        u = min(stop, item + r.nu);
+        const uint32_t tile1 = u - item - ITEM_COST;
         const uint32_t n_tiles = tile1 - tile0;
         const uint32_t len = r.len, cached = r.cached;
         const uint32_t table_row = r.b * a.L.max_pages;   // checked on the host: below 2^32
@@ -433,6 +474,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 #pragma unroll
             for (int s = 0; s < KEPT; ++s)
                 q[s] = as_bf16x8(ld16(src + s * 32));
+            if (flip)
+#pragma unroll
+                for (int s = 0; s < KEPT; ++s)
+                    q[s] = as_bf16x8(__builtin_bit_cast(u32x4, q[s]) ^ flip);
             if constexpr (FP8) {
 #pragma unroll
                 for (int s0 = KEPT; s0 < D / 16; s0 += 7) {
@@ -442,7 +487,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                         v[s] = ld16(src + (s0 + s) * 32);
 #pragma unroll
                     for (int s = 0; s < 7; ++s)
-                        lds_st16(my_q + (s0 + s - KEPT) * 1024, v[s]);
+                        lds_st16(my_q + (s0 + s - KEPT) * 1024, v[s] ^ flip);
                 }
             }
         }
@@ -511,34 +556,31 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             if constexpr (FP8)
                 scale_dst = lds0 + SCALES_AT + (t & (STAGES - 1)) * SCALES + wave * SCALES_WAVE;
         };
-        auto load = [&](int j) __attribute__((always_inline)) {
-            if constexpr (FP8) {
-                if (j == 5) {         // lane l: scale of block l / 8 of row l % 8
-                    if constexpr (PAGE8)
-                        load_lds4(scale_src, scale_off, scale_dst, src_on, src_on & 0xFFu);
-                    else
-                        load_lds4(scale_src, scale_dst, src_on, src_on & 0xFFu);
-                    return;
+        // Its loads in GROUPS groups.
+        auto load = [&](auto group) __attribute__((always_inline)) {
+            constexpr int g = group;
+            if constexpr (FP8 && g == 2) {
+                // Lanes 0 .. 31: the last 64 codes of row l / 4; then lane l: scale of block l / 8 of row l % 8.
+                const uint32_t to = dst - wave * 512 + 4 * BLOCK_BYTES;
+                if constexpr (PAGE8) {
+                    load_lds<0, 1>(src_base, src_off4, to, src_on, 0);
+                    load_lds4(scale_src, scale_off, scale_dst, src_on, src_on & 0xFFu);
+                } else {
+                    load_lds<0, 1>(src_base4, to, src_on, 0);
+                    load_lds4(scale_src, scale_dst, src_on, src_on & 0xFFu);
                 }
-                if (j == 4) {         // lanes 0 .. 31: the last 64 codes of row l / 4
-                    const uint32_t to = dst - wave * 512 + 4 * BLOCK_BYTES;
-                    if constexpr (PAGE8)
-                        load_lds(src_base, src_off4, to, src_on, 0);
-                    else
-                        load_lds(src_base4, to, src_on, 0);
-                    return;
-                }
+            } else {
+                constexpr int n = FP8 ? 2 : 3;
+                if constexpr (PAGE8)
+                    load_lds<g * n, n>(src_base, src_off, dst, src_on, src_on);
+                else
+                    load_lds<g * n, n>(src_base, dst, src_on, src_on);
             }
-            if constexpr (PAGE8)
-                load_lds(src_base, src_off + j * 128, dst + j * BLOCK_BYTES, src_on, src_on);
-            else
-                load_lds(src_base + j * 128, dst + j * BLOCK_BYTES, src_on, src_on);
         };
+        constexpr int GROUPS = 3;
         auto issue = [&](uint32_t t) __attribute__((always_inline)) {
             locate(t);
-#pragma unroll
-            for (int j = 0; j < LOADS; ++j)
-                load(j);
+            each<GROUPS>(load);
         };
         // e4m3: scales of block b of the rows 8 i + 4 half .. + 3 of a tile.
         auto scales_at = [&](uint32_t t) __attribute__((always_inline)) {
@@ -572,7 +614,6 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             else
                 wait_loads<0>();
             lds_barrier();
-            locate(t + 3);
             const uint32_t p0 = (tile0 + t) * TILE;
             const bool masked = p0 + TILE > cached;
             if (masked && (r.n > 1 || a.mask)) {
@@ -637,9 +678,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             // No query rows for this wave: it only loads.
             for (uint32_t t = 0; t < n_tiles; ++t) {
                 enter(t);
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j)
-                    load(j);
+                issue(t + 3);
                 if constexpr (PAGE8)
                     next_id = id_at(entry_of(t + 4));
             }
@@ -695,7 +734,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 if (at == 0)
                     mfma_first<FP8>(sum, x, y);
                 else if (end)
-                    mfma_last<FP8>(sum, x, y);
+                    sum = mfma_last<FP8>(sum, x, y);
                 else
                     mfma_next<FP8>(sum, x, y);
                 if constexpr (k + KD < KN)
@@ -719,13 +758,12 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             });
             return acc;
         };
-        float s[16];        // scores of the tile at hand, in units of log2
+        // Scores of the tile at hand, their maximum (in units of log2, as mref), and whether the
+        // reference lags too far behind it anywhere.
+        f32x16 s;
         float mx;
-        auto scaled_max = [&](const f32x16& raw, int i) __attribute__((always_inline)) {
-            s[i] = raw[i] * c;
-            mx = i == 0 ? s[0] : fmaxf(mx, s[i]);
-        };
-        // Masks the scores of tile t, and moves the reference maximum if it lags too far.
+        uint64_t lagging;
+        // Masks the scores of tile t if they have to be, and moves the reference if it lags.
         auto settle = [&](uint32_t t) __attribute__((always_inline)) {
             const uint32_t p0 = (tile0 + t) * TILE;
             if (p0 + TILE > cached) {
@@ -736,9 +774,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     s[i] = (seen >> (8 * (i >> 2) + 4 * half + (i & 3))) & 1 ? s[i] : -INFINITY;
                     mx = fmaxf(mx, s[i]);
                 }
-                mx = fmaxf(mx, swap32(mx));
+                mx = fmaxf(mx, swap32(mx)) * c;
+                lagging = __ballot(mx > mref + kSlack);
             }
-            if (__ballot(mx > mref + kSlack)) {
+            if (lagging) {
                 const float next = fmaxf(mref, mx);
                 const float keep = next == mref ? 1.0f : __builtin_amdgcn_exp2f(mref - next);
                 mref = next;
@@ -752,11 +791,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             }
         };
         {
-            const f32x16 raw = scores(0, [](auto) {});
+            s = scores(0, [](auto) {});
+            mx = s[0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                scaled_max(raw, i);
-            mx = fmaxf(mx, swap32(mx));
+            for (int i = 1; i < 16; ++i)
+                mx = fmaxf(mx, s[i]);
+            mx = fmaxf(mx, swap32(mx)) * c;
+            lagging = __ballot(mx > mref + kSlack);
             settle(0);
         }
 
@@ -782,8 +823,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             [[maybe_unused]] float e[16];
             Frag vf[VD];
             auto weights = [&](int k) __attribute__((always_inline)) {
-                const float e0 = __builtin_amdgcn_exp2f(s[2 * k] - ref);
-                const float e1 = __builtin_amdgcn_exp2f(s[2 * k + 1] - ref);
+                const float e0 = __builtin_amdgcn_exp2f(fmaf(s[2 * k], c, -ref));
+                const float e1 = __builtin_amdgcn_exp2f(fmaf(s[2 * k + 1], c, -ref));
                 sum += e0 + e1;
                 if constexpr (FP8) {
                     e[2 * k] = e0;
@@ -792,7 +833,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     pk[k] = pack_bf16x2(e0, e1);
                 }
             };
-            const f32x16 raw = scores(t + 1, [&](auto index) __attribute__((always_inline)) {
+            const f32x16 next_s = scores(t + 1, [&](auto index) __attribute__((always_inline)) {
                 constexpr int k = index;
                 if constexpr (k < 0) {
                     weights(0);
@@ -800,12 +841,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 } else if constexpr (FP8 ? k < 6 : k % 3 == 0 && k / 3 < 6) {
                     weights(2 + (FP8 ? k : k / 3));
                 }
-                if constexpr (k >= 0 && k % 4 == 1 && k / 4 < LOADS)
-                    load(k / 4);
+                if constexpr (k == 4)
+                    locate(t + 3);
                 if constexpr (k >= KN - VD)
                     vf[k - (KN - VD)] = vfrag(k - (KN - VD));
             });
             l += sum;
+            s = next_s;
             // e4m3: the weights times the scales of one block of 128 features at a time, rounded
             // to bf16 once.
             bf16x8 pf[2];
@@ -831,10 +873,14 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of_codes(vf[v % VD]), pf[v & 1], o[v >> 1], 0, 0, 0);
                 if constexpr (v + VD < VN)
                     vf[v % VD] = vfrag(v + VD);
-                if constexpr (v >= 4 && v < 20)
-                    scaled_max(raw, v - 4);
+                if constexpr (v % 8 == 3 && v / 8 < GROUPS)
+                    load(std::integral_constant<int, v / 8>{});
+                if constexpr (v >= 4 && v < 20 && v % 2 == 0)
+                    mx = v == 4 ? fmaxf(s[0], s[1]) : fmaxf(fmaxf(mx, s[v - 4]), s[v - 3]);
                 if constexpr (v == 20)
-                    mx = fmaxf(mx, swap32(mx));
+                    mx = fmaxf(mx, swap32(mx)) * c;
+                if constexpr (v == 22)
+                    lagging = __ballot(mx > mref + kSlack);
                 if constexpr (PAGE8 && v == 24)
                     next_entry = entry_of(t + 4);
                 if constexpr (FP8) {
@@ -854,7 +900,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         }
 
         l += swap32(l);
-        if (tile0 == 0 && tile1 == r.nt) {
+        if (tile0 == 0 && tile1 + ITEM_COST == r.nu) {
             const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
             store_row(static_cast<uint16_t*>(a.out) + (int64_t)qrow * K, o, inv, valid, half);
             if (a.lse && valid && half == 0)
@@ -1054,11 +1100,11 @@ __global__ void __launch_bounds__(256) tree_attention_join(MfmaParams P)
 
 bool tree_attention_mfma_fits(const TreeAttentionArgs& a, AttnKind kind)
 {
-    return (kind == ATTN_BF16 || kind == ATTN_E4M3) && a.D == D && a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
+    return (kind == ATTN_BF16 || kind == ATTN_E4M3) && a.scale != 0.0f && a.D == D && a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
            (kind == ATTN_BF16 || a.Ls.stride_token < (int64_t(1) << 28)) &&
            (uint64_t)a.L.batch * a.L.max_pages < (uint64_t(1) << 32) &&
-           // items (at most one partly filled per request) times tiles
-           ((uint64_t)a.T * a.H / kAttnRows + std::min<uint64_t>(a.L.batch, a.T)) * (a.capacity / TILE + 1) <
+           // items (at most one partly filled per request) times units
+           ((uint64_t)a.T * a.H / kAttnRows + std::min<uint64_t>(a.L.batch, a.T)) * (a.capacity / TILE + 1 + ITEM_COST) <
                (uint64_t(1) << 31);
 }
 
