@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 from typing import Optional
@@ -98,6 +99,8 @@ _lib = None
 def lib():
     """The loaded C library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -205,30 +208,25 @@ class PagedKVCache:
     scale_granularity: int = 128
 
     def descriptor(self) -> CacheDesc:
-        import torch
         p = self.pool
         if p.dim() != 6:
             raise ValueError("pool must be [pages, layers, kv, page_size, heads, head_dim]")
-        if p.stride(5) != 1 or p.stride(4) != p.shape[5]:
+        pages, layers, kv, page_size, heads, head_dim = p.shape
+        sp, sl, sk, st, sh, se = p.stride()
+        if se != 1 or sh != head_dim:
             raise ValueError("token rows of the pool must be contiguous")
-        dt = {torch.float32: MLA_DTYPE_F32, torch.bfloat16: MLA_DTYPE_BF16, torch.uint8: MLA_DTYPE_F8E4M3FN,
-              torch.float8_e4m3fn: MLA_DTYPE_F8E4M3FN}.get(p.dtype, -1)
-        d = CacheDesc()
-        d.blocks = p.data_ptr()
-        d.dtype = dt
-        d.num_pages, d.num_layers, d.num_kv, d.page_size, d.num_heads, d.head_dim = p.shape
-        d.stride_page, d.stride_layer, d.stride_kv, d.stride_token = p.stride(0), p.stride(1), p.stride(2), p.stride(3)
         pt = self.page_table
         if pt.dim() != 2 or not pt.is_contiguous() or pt.element_size() != 4:
             raise ValueError("page_table must be a contiguous 32-bit [batch, max_pages] tensor")
-        d.page_table = pt.data_ptr()
-        d.batch_size, d.max_pages_per_seq = pt.shape
+        batch, max_pages = pt.shape
+        lengths = None
         if self.cache_lengths is not None:
             cl = self.cache_lengths
-            if not cl.is_contiguous() or cl.element_size() != 4 or cl.numel() != pt.shape[0]:
+            if not cl.is_contiguous() or cl.element_size() != 4 or cl.numel() != batch:
                 raise ValueError("cache_lengths must be a contiguous 32-bit [batch] tensor")
-            d.cache_lengths = cl.data_ptr()
-        return d
+            lengths = cl.data_ptr()
+        return CacheDesc(p.data_ptr(), _pool_dtypes().get(p.dtype, -1), layers, pages, page_size, kv, heads, head_dim,
+                         sp, sl, sk, st, pt.data_ptr(), batch, max_pages, lengths)
 
     def scales_descriptor(self) -> ScalesDesc:
         import torch
@@ -248,18 +246,11 @@ class PagedKVCache:
 
 def _stream(stream):
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
-def _on_device(t, what):
-    """Device pointer of a tensor that lives on the current GPU; anything else
-    (a host tensor, another GPU's tensor) is refused before any launch."""
-    import torch
-    if t is None or not isinstance(t, torch.Tensor) or not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} must be a tensor on the current GPU")
-    return t.data_ptr()
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # torch.cuda.current_stream() without the Stream object around the handle: it costs more
+    # than a small call's kernel.
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _nbytes(t):
@@ -290,16 +281,31 @@ def _u32(t, what, entries=0):
 
 
 def _gpu(**tensors):
-    """Every tensor a call hands to the library must be on the current GPU."""
+    """Every tensor a call hands to the library must live on the current GPU; anything
+    else (a host tensor, another GPU's tensor) is refused before any launch."""
+    import torch
+    current = None
     for name, t in tensors.items():
-        if t is not None:
-            _on_device(t, name)
+        if t is None:
+            continue
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if current is None:
+                current = torch.cuda.current_device()
+            if t.get_device() == current:
+                continue
+        raise ValueError(f"{name} must be a tensor on the current GPU")
 
 
+@functools.lru_cache(maxsize=None)
 def _dtypes():
     import torch
     return {MLA_DTYPE_F32: (torch.float32,), MLA_DTYPE_BF16: (torch.bfloat16,),
             MLA_DTYPE_F8E4M3FN: (torch.uint8, torch.float8_e4m3fn)}
+
+
+@functools.lru_cache(maxsize=None)
+def _pool_dtypes():
+    return {dtype: code for code, dtypes in _dtypes().items() for dtype in dtypes}
 
 
 def _bytes_of(dtype_code):
