@@ -59,7 +59,8 @@ struct MfmaParams {
     uint32_t ps_magic, ps_shift;             // p / page_size = mulhi(p, magic) >> shift for p < 2^31
     uint32_t piece;                          // floats of a partial result slot
     Cut* cuts;                               // [kAttnGroups]
-    int min_tiles;                           // least tiles of a workgroup's share
+    uint32_t groups;                         // of 32 rows in an item: 4, or 2
+    int min_tiles;                           // least steps of a workgroup's share
 };
 
 __device__ inline uint64_t uniform(uint64_t v)
@@ -69,15 +70,25 @@ __device__ inline uint64_t uniform(uint64_t v)
 }
 __device__ inline uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
 
-// Rows of a request and its share of the work: nm items of 128 query rows.  An item counts as
-// ITEM_COST units before its tiles' one each: fetching its queries, filling the ring and
-// writing its results takes about as long as that many tiles.
-constexpr uint32_t ITEM_COST = 8;
+// How a workgroup's four waves share an item.  SPLIT 1: 128 query rows, 32 per wave, every wave
+// reads all tiles.  SPLIT 2: 64 query rows, two pairs of waves; a step takes two tiles, one per
+// pair, and the pairs' results are joined at the end.  An item counts as COST units before its
+// steps' one each: fetching its queries, filling the ring and writing its results takes about as
+// long as that many steps.
+template <int SPLIT>
+struct Shape {
+    static constexpr uint32_t ROWS = kAttnRows / SPLIT;   // query rows of an item
+    static constexpr uint32_t STEP = TILE * SPLIT;        // cache rows of a step
+    static constexpr uint32_t COST = 8;
+};
+
+// Rows of a request and its share of the work: nm items.
 struct Request {
-    uint32_t b, t0, n, cached, len, nm, nu;  // nu = ITEM_COST + tiles
+    uint32_t b, t0, n, cached, len, nm, nu;  // nu = COST + steps
     uint32_t base;                           // units of all requests before it
 };
 
+template <int SPLIT>
 __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
 {
     Request r{};
@@ -88,8 +99,8 @@ __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
     r.n = t1 > r.t0 ? t1 - r.t0 : 0;
     r.cached = min(a.cache_len[b], a.capacity);
     r.len = min(r.cached + r.n, a.capacity);
-    r.nm = (r.n * (uint32_t)a.H + kAttnRows - 1) / kAttnRows;   // n * H below 2^31 / D
-    r.nu = (r.len + TILE - 1) / TILE + ITEM_COST;
+    r.nm = (r.n * (uint32_t)a.H + Shape<SPLIT>::ROWS - 1) / Shape<SPLIT>::ROWS;   // n * H below 2^31 / D
+    r.nu = (r.len + Shape<SPLIT>::STEP - 1) / Shape<SPLIT>::STEP + Shape<SPLIT>::COST;
     return r;
 }
 
@@ -114,7 +125,9 @@ __device__ inline uint32_t wave_inclusive(uint32_t v, int lane)
 // cut that falls within `snap` tiles of an item's first or last one is moved there: the item
 // is then not split for so little.  Every wave works it out for itself; the requests of the last 64
 // looked at stay in its lanes.  The host has checked that the units number below 2^31.
+template <int SPLIT>
 struct Schedule {
+    static constexpr uint32_t COST = Shape<SPLIT>::COST;
     const TreeAttentionArgs& a;
     int lane;
     uint32_t total, groups, share, rest, snap;
@@ -129,7 +142,7 @@ struct Schedule {
         before = tiles_before;
         mine = Request{};
         if (b0 + lane < a.L.batch)
-            mine = request_at(a, b0 + lane);
+            mine = request_at<SPLIT>(a, b0 + lane);
         scan = wave_inclusive(mine.nm * mine.nu, lane);
     }
     __device__ uint32_t loaded() const { return (uint32_t)__builtin_amdgcn_readlane((int)scan, 63); }
@@ -182,7 +195,7 @@ struct Schedule {
         const uint32_t x = raw(w);
         r = find(x);
         const uint32_t lo = r.base + (x - r.base) / r.nu * r.nu;
-        return x - lo <= ITEM_COST + snap ? lo : lo + r.nu - x <= snap ? lo + r.nu : x;
+        return x - lo <= COST + snap ? lo : lo + r.nu - x <= snap ? lo + r.nu : x;
     }
 };
 
@@ -349,36 +362,63 @@ __device__ inline bf16x8 bf16_of_codes(bf16x8 v) { return v; }
 
 __device__ inline bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
-// Final output of one lane pair's row: eight features per 16-byte store.
-__device__ inline void store_row(uint16_t* out, const f32x16 (&o)[16], float inv, bool valid, int half)
+// The result of one lane pair's row, feature blocks FIRST .. FIRST + N - 1: the final output,
+// eight features per 16-byte store, or a share's sums, maximum and sum as they are, in lane order.
+template <int FIRST, int N>
+__device__ __attribute__((always_inline)) inline void store_result(const TreeAttentionArgs& a, const f32x16 (&o)[16],
+                                                                   float mref, float l, uint32_t qrow, bool valid,
+                                                                   bool whole, float* piece, int lane)
 {
+    const int half = lane >> 5, col = lane & 31;
+    if (whole) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)qrow * K + 8 * half;
 #pragma unroll
-    for (int fb = 0; fb < 16; ++fb)
+        for (int fb = FIRST; fb < FIRST + N; ++fb)
 #pragma unroll
-        for (int i = 0; i < 16; i += 8) {
-            uint32_t x0 = pack_bf16x2(o[fb][i] * inv, o[fb][i + 1] * inv);
-            uint32_t x1 = pack_bf16x2(o[fb][i + 2] * inv, o[fb][i + 3] * inv);
-            uint32_t y0 = pack_bf16x2(o[fb][i + 4] * inv, o[fb][i + 5] * inv);
-            uint32_t y1 = pack_bf16x2(o[fb][i + 6] * inv, o[fb][i + 7] * inv);
-            const auto a = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-            const auto b = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-            if (valid)
-                st16(out + fb * 32 + 2 * i + 8 * half, u32x4{a[0], b[0], a[1], b[1]});
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < 16; i += 8) {
+                uint32_t x0 = pack_bf16x2(o[fb][i] * inv, o[fb][i + 1] * inv);
+                uint32_t x1 = pack_bf16x2(o[fb][i + 2] * inv, o[fb][i + 3] * inv);
+                uint32_t y0 = pack_bf16x2(o[fb][i + 4] * inv, o[fb][i + 5] * inv);
+                uint32_t y1 = pack_bf16x2(o[fb][i + 6] * inv, o[fb][i + 7] * inv);
+                const auto u = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+                const auto v = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+                if (valid)
+                    st16(out + fb * 32 + 2 * i, u32x4{u[0], v[0], u[1], v[1]});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        if (FIRST == 0 && a.lse && valid && half == 0)
+            a.lse[qrow] = l == 0.0f ? -INFINITY : mref * kLn2 + __logf(l);
+    } else {
+#pragma unroll
+        for (int fb = FIRST; fb < FIRST + N; ++fb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                *reinterpret_cast<f32x4*>(piece + ((fb * 4 + i) * 64 + lane) * 4) =
+                    f32x4{o[fb][4 * i], o[fb][4 * i + 1], o[fb][4 * i + 2], o[fb][4 * i + 3]};
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        if (FIRST == 0 && half == 0) {
+            piece[32 * K + col] = mref;
+            piece[32 * K + 32 + col] = l;
         }
+    }
 }
 
-template <bool PAGE8, bool FP8>
+template <bool PAGE8, bool FP8, int SPLIT>
 __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams P)
 {
     __shared__ __attribute__((aligned(1024))) char smem[FP8 ? SMEM8 : STAGES * STAGE];
-    constexpr int LOADS = FP8 ? 6 : BLOCKS;   // LDS loads per wave and tile
+    constexpr int LOADS = FP8 ? 6 : BLOCKS;   // LDS loads of 8 rows
+    constexpr uint32_t ROWS = Shape<SPLIT>::ROWS, STEP = Shape<SPLIT>::STEP, COST = Shape<SPLIT>::COST;
     const TreeAttentionArgs& a = P.a;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, col = lane & 31;
+    // The wave's 32 query rows, and its tile of each step.
+    const uint32_t qwave = SPLIT == 1 ? wave : wave & 1, pair = SPLIT == 1 ? 0 : wave >> 1;
 
-    Schedule sched(a, lane, P.min_tiles);
+    Schedule<SPLIT> sched(a, lane, P.min_tiles);
     // Neighbouring shares go to one XCD (block i runs on XCD i % 8): items of one request
     // then read the same rows through one L2.
     const uint32_t per = (sched.groups + 7) / 8;
@@ -394,9 +434,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         if (u == sched.raw(w)) {
             const uint32_t m = (u - r.base) / r.nu, lo = r.base + m * r.nu;
             if (u != lo)   // (an end of an item may be a cut, within `snap` of it)
-                rec = Cut{w, sched.first_cut_past(lo + ITEM_COST + sched.snap),
+                rec = Cut{w, sched.first_cut_past(lo + COST + sched.snap),
                           sched.first_cut_past(lo + r.nu - sched.snap - 1) - 1,
-                          r.t0 * (uint32_t)a.H + m * kAttnRows, r.n * (uint32_t)a.H - m * kAttnRows, {}};
+                          r.t0 * (uint32_t)a.H + m * ROWS, r.n * (uint32_t)a.H - m * ROWS, {}};
         }
     }
     if (threadIdx.x == 0)
@@ -437,34 +477,40 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         return vrow * 128 + (c16 & 1) * 8 + (((ln >> 4 & 1) ^ f(vrow)) * 16);
     };
     const uint32_t lds0 = lds_addr(smem);
-    // Stage of tile t (the tiles of an item counted from 0).
-    auto stage_of = [](uint32_t t) __attribute__((always_inline)) { return (t & (STAGES - 1)) * (FP8 ? STAGE8 : STAGE); };
+    // Stage of the wave's tile of step t (the steps of an item counted from 0).
+    auto stage_no = [=](uint32_t t) __attribute__((always_inline)) {
+        return SPLIT == 1 ? t & (STAGES - 1) : (t & 1) * 2 + pair;
+    };
+    auto stage_of = [=](uint32_t t) __attribute__((always_inline)) { return stage_no(t) * (FP8 ? STAGE8 : STAGE); };
     const float c = fabsf(a.scale) * kLog2e;   // a negative scale turns the queries' signs; 0 is not taken
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 
     while (u < stop) {
         while (u >= r.base + r.nm * r.nu) {
             const uint32_t next = r.base + r.nm * r.nu;
-            r = request_at(a, r.b + 1);
+            r = request_at<SPLIT>(a, r.b + 1);
             r.base = next;
             r = uniform(r);
         }
         const uint32_t m = uniform((u - r.base) / r.nu);
         const uint32_t item = r.base + m * r.nu;
-        const uint32_t tile0 = u - item < ITEM_COST ? 0 : u - item - ITEM_COST;
+        const uint32_t tile0 = u - item < COST ? 0 : u - item - COST;
         u = min(stop, item + r.nu);
-        const uint32_t tile1 = u - item - ITEM_COST;
+        const uint32_t tile1 = u - item - COST;
         const uint32_t n_tiles = tile1 - tile0;
         const uint32_t len = r.len, cached = r.cached;
         const uint32_t table_row = r.b * a.L.max_pages;   // checked on the host: below 2^32
 
         const uint32_t rows = r.n * (uint32_t)a.H;                 // below 2^31 / D
-        const uint32_t row = m * kAttnRows + wave * 32 + col;
-        const bool live = uniform(m * kAttnRows + wave * 32) < rows;
+        const uint32_t row = m * ROWS + qwave * 32 + col;
+        const bool live = uniform(m * ROWS + qwave * 32) < rows;
         const bool valid = row < rows;
         const uint32_t qrow = r.t0 * (uint32_t)a.H + min(row, rows - 1);
         const uint32_t tok = min(row, rows - 1) / (uint32_t)a.H;   // token of the request
 
+        // SPLIT 2: the join of the item before is done with LDS, the queries' part included.
+        if (SPLIT == 2)
+            lds_barrier();
         // Query fragments: lane holds features 16 s + 8 half .. + 7 of its row.
         constexpr int KEPT = FP8 ? QUERY_KEPT : D / 16;
         bf16x8 q[KEPT];
@@ -493,21 +539,24 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         }
         // The stages of the item before are no longer read (and no load into them is in flight:
         // the last step waited for all of them, and those behind the last tile are switched off).
-        lds_barrier();
+        if (SPLIT == 1)
+            lds_barrier();
 
-        // Loads of one tile: this wave fetches rows 8 wave .. 8 wave + 7, lane l granule l % 8
-        // of every block of row l / 8.  Rows past the end repeat the last one.
+        // Loads of one tile: this wave fetches rows 8 i .. 8 i + 7 for its one or two bands i,
+        // lane l granule l % 8 of every block of row l / 8.  Rows past the end repeat the last one.
         // The page id of a tile's rows (PAGE8: 8 rows starting at a multiple of 8 are in one page)
         // is asked for one tile early, when no LDS read is outstanding: a scalar load makes every
         // wait for LDS reads wait for all of them.
-        [[maybe_unused]] uint32_t next_id = 0;
-        [[maybe_unused]] const uint32_t* next_entry = a.L.page_table;
-        auto group_start = [&](uint32_t t) __attribute__((always_inline)) {
-            const uint32_t p0 = (tile0 + t) * TILE + wave * 8;
+        [[maybe_unused]] uint32_t next_id[SPLIT] = {};
+        [[maybe_unused]] const uint32_t* next_entry[SPLIT] = {};
+        auto band = [&](int i) __attribute__((always_inline)) { return SPLIT * qwave + i; };
+        auto tile_start = [&](uint32_t t) __attribute__((always_inline)) { return (tile0 + t) * STEP + pair * TILE; };
+        auto group_start = [&](uint32_t t, int i) __attribute__((always_inline)) {
+            const uint32_t p0 = tile_start(t) + band(i) * 8;
             return p0 < len ? p0 : (len - 1) & ~7u;
         };
-        auto entry_of = [&](uint32_t t) __attribute__((always_inline)) {
-            const uint32_t lp = __umulhi(group_start(t), P.ps_magic) >> P.ps_shift;
+        auto entry_of = [&](uint32_t t, int i) __attribute__((always_inline)) {
+            const uint32_t lp = __umulhi(group_start(t, i), P.ps_magic) >> P.ps_shift;
             return a.L.page_table + table_row + min(lp, a.L.max_pages - 1);
         };
         auto id_at = [&](const uint32_t* entry) __attribute__((always_inline)) {
@@ -522,16 +571,16 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         [[maybe_unused]] const char* src_base4 = nullptr;
         uint32_t last_tile = n_tiles;
         asm("" : "+s"(last_tile));   // the switch below stays scalar arithmetic
-        auto locate = [&](uint32_t t) __attribute__((always_inline)) {
+        auto locate = [&](uint32_t t, int i) __attribute__((always_inline)) {
             src_on = (uint32_t)((int32_t)(t - last_tile) >> 31);   // all ones while t < n_tiles
-            dst = lds0 + stage_of(t) + wave * 1024;
+            dst = lds0 + stage_of(t) + band(i) * 1024;
             const uint32_t ln = lane_again();
-            const uint32_t load_off = ((ln & 7) ^ f(wave * 8 + (ln >> 3))) * 16;
-            [[maybe_unused]] const uint32_t load_off4 = 512 + ((ln ^ (2 * wave + (ln >> 4))) & 3) * 16;
+            const uint32_t load_off = ((ln & 7) ^ f(band(i) * 8 + (ln >> 3))) * 16;
+            [[maybe_unused]] const uint32_t load_off4 = 512 + ((ln ^ (2 * band(i) + (ln >> 4))) & 3) * 16;
             if constexpr (PAGE8) {
-                const uint32_t pg = group_start(t);
+                const uint32_t pg = group_start(t, i);
                 const uint32_t slot = pg - (__umulhi(pg, P.ps_magic) >> P.ps_shift) * a.L.page_size;
-                const uint32_t id = min(next_id, a.L.num_pages - 1);
+                const uint32_t id = min(next_id[i], a.L.num_pages - 1);
                 src_base = a.L.base + (int64_t)id * a.L.stride_page + (int64_t)slot * a.L.stride_token;
                 const uint32_t last = len - 1 - pg;
                 src_off = min(ln >> 3, last) * (uint32_t)a.L.stride_token + load_off;
@@ -542,7 +591,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 }
             } else {
                 auto at = [&](const PagedLayer& L, uint32_t row) __attribute__((always_inline)) {
-                    const uint32_t p = min((tile0 + t) * TILE + wave * 8 + row, len - 1);
+                    const uint32_t p = min(tile_start(t) + band(i) * 8 + row, len - 1);
                     const uint32_t lp = p / L.page_size;
                     const uint32_t id = min(L.page_table[table_row + min(lp, L.max_pages - 1)], L.num_pages - 1);
                     return L.base + (int64_t)id * L.stride_page + (int64_t)(p - lp * L.page_size) * L.stride_token;
@@ -554,14 +603,14 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 }
             }
             if constexpr (FP8)
-                scale_dst = lds0 + SCALES_AT + (t & (STAGES - 1)) * SCALES + wave * SCALES_WAVE;
+                scale_dst = lds0 + SCALES_AT + stage_no(t) * SCALES + band(i) * SCALES_WAVE;
         };
         // Its loads in GROUPS groups.
-        auto load = [&](auto group) __attribute__((always_inline)) {
+        auto load = [&](auto group, int i) __attribute__((always_inline)) {
             constexpr int g = group;
             if constexpr (FP8 && g == 2) {
                 // Lanes 0 .. 31: the last 64 codes of row l / 4; then lane l: scale of block l / 8 of row l % 8.
-                const uint32_t to = dst - wave * 512 + 4 * BLOCK_BYTES;
+                const uint32_t to = dst - band(i) * 512 + 4 * BLOCK_BYTES;
                 if constexpr (PAGE8) {
                     load_lds<0, 1>(src_base, src_off4, to, src_on, 0);
                     load_lds4(scale_src, scale_off, scale_dst, src_on, src_on & 0xFFu);
@@ -579,49 +628,64 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         };
         constexpr int GROUPS = 3;
         auto issue = [&](uint32_t t) __attribute__((always_inline)) {
-            locate(t);
-            each<GROUPS>(load);
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i) {
+                locate(t, i);
+                each<GROUPS>([&](auto group) __attribute__((always_inline)) { load(group, i); });
+            }
         };
         // e4m3: scales of block b of the rows 8 i + 4 half .. + 3 of a tile.
         auto scales_at = [&](uint32_t t) __attribute__((always_inline)) {
-            return SCALES_AT + (t & (STAGES - 1)) * SCALES + (lane_again() >> 5) * 16;
+            return SCALES_AT + stage_no(t) * SCALES + (lane_again() >> 5) * 16;
         };
         auto scales_of = [&](uint32_t at, int b, int i) __attribute__((always_inline)) {
             return *reinterpret_cast<const f32x4*>(smem + at + i * SCALES_WAVE + b * 32);
         };
 
-        uint32_t id2 = 0, id3 = 0;
-        if constexpr (PAGE8) {
-            const uint32_t id0 = id_at(entry_of(0)), id1 = id_at(entry_of(1));
-            id2 = id_at(entry_of(2));
-            id3 = id_at(entry_of(3));
-            next_id = id0;
-            issue(0);
-            next_id = id1;
-        } else {
-            issue(0);
+        // Steps loaded ahead of the first; then step t loads step t + AHEAD.
+        constexpr int FIRST = SPLIT == 1 ? 3 : 2, AHEAD = SPLIT == 1 ? 3 : 1;
+        {
+            constexpr int IDS = AHEAD + 1;
+            uint32_t ids[IDS][SPLIT] = {};
+            if constexpr (PAGE8)
+#pragma unroll
+                for (int t = 0; t < IDS; ++t)
+#pragma unroll
+                    for (int i = 0; i < SPLIT; ++i)
+                        ids[t][i] = id_at(entry_of(t, i));
+#pragma unroll
+            for (int t = 0; t < IDS; ++t) {
+#pragma unroll
+                for (int i = 0; i < SPLIT; ++i)
+                    next_id[i] = ids[t][i];
+                if (t < FIRST)
+                    issue(t);
+            }
         }
-        issue(1);
-        next_id = id2;
-        issue(2);
-        next_id = id3;
+        auto locate_next = [&](uint32_t t) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i)
+                next_entry[i] = entry_of(t + AHEAD + 1, i);
+        };
+        // Ids for the loads of the next step, once `next_entry` has their places.
+        auto next_ids = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < SPLIT; ++i)
+                next_id[i] = id_at(next_entry[i]);
+        };
 
-        // Start of step t: tile t + 1 is there for every wave and every wave is done with tile
-        // t - 1, whose stage takes tile t + 3.
-        auto enter = [&](uint32_t t) __attribute__((always_inline)) {
-            if (t + 2 < n_tiles)
-                wait_loads<LOADS>();
-            else
-                wait_loads<0>();
-            lds_barrier();
-            const uint32_t p0 = (tile0 + t) * TILE;
-            const bool masked = p0 + TILE > cached;
-            if (masked && (r.n > 1 || a.mask)) {
-                // Drafted rows may be hidden from some tokens and hold anything: a weight of 0
-                // would turn their infinities and NaN into NaN, so those become 0 here (a token
-                // that sees such a row has a NaN weight for it already).
-                char* mine = smem + stage_of(t) + wave * 1024 + lane * 16;
-                if (p0 + wave * 8 + (lane >> 3) >= cached)
+        // Drafted rows may be hidden from some tokens and hold anything: a weight of 0 would turn
+        // their infinities and NaN into NaN, so those become 0 here, between the scores and the
+        // weighted sums of step t (a token that sees such a row has a NaN weight for it already).
+        auto clear_nonfinite = [&](uint32_t t) __attribute__((always_inline)) {
+            if ((tile0 + t + 1) * STEP <= cached || !(r.n > 1 || a.mask))
+                return;
+            if (SPLIT == 2)
+                lds_barrier();   // the scores are done
+            const uint32_t p0 = tile_start(t);
+            for (int i = 0; i < SPLIT; ++i) {
+                char* mine = smem + stage_of(t) + band(i) * 1024 + lane * 16;
+                if (p0 + band(i) * 8 + (lane >> 3) >= cached)
                     for (int j = 0; j < K / (FP8 ? 128 : 64); ++j) {
                         u32x4 v = lds_ld16(mine + j * BLOCK_BYTES);
 #pragma unroll
@@ -636,15 +700,30 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                         }
                         lds_st16(mine + j * BLOCK_BYTES, v);
                     }
-                if (FP8 && lane < 40 && p0 + wave * 8 + (lane & 7) >= cached) {
-                    float* sc = reinterpret_cast<float*>(smem + SCALES_AT + (t & (STAGES - 1)) * SCALES + wave * SCALES_WAVE) + lane;
+                if (FP8 && lane < 40 && p0 + band(i) * 8 + (lane & 7) >= cached) {
+                    float* sc = reinterpret_cast<float*>(smem + SCALES_AT + stage_no(t) * SCALES + band(i) * SCALES_WAVE) + lane;
                     *sc = fabsf(*sc) < INFINITY ? *sc : 0.0f;
                 }
-                lds_barrier();
             }
+            lds_barrier();
+        };
+
+        // Start of step t.  SPLIT 1: tile t + 1 is there for every wave and every wave is done with
+        // tile t - 1, whose stage takes tile t + 3.  SPLIT 2: the tiles of step t are there, and
+        // those of step t + 1 take the place of those of step t - 1 (step 0: they are on their way).
+        auto enter = [&](uint32_t t) __attribute__((always_inline)) {
+            if (SPLIT == 1 ? t + 2 < n_tiles : t == 0 && n_tiles > 1)
+                wait_loads<SPLIT * LOADS>();
+            else
+                wait_loads<0>();
+            lds_barrier();
+            if (SPLIT == 1)
+                clear_nonfinite(t);
         };
         // Bits of the tile's rows that this lane's token sees.
         auto seen_rows = [&](uint32_t p0) __attribute__((always_inline)) {
+            if (SPLIT == 2 && p0 >= len)
+                return 0u;
             const uint32_t room = min(len - p0, (uint32_t)TILE);
             uint32_t seen;
             if (a.mask) {
@@ -667,20 +746,31 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             return seen & (room >= 32 ? ~0u : (1u << room) - 1);
         };
 
-        if (n_tiles > 2)
-            wait_loads<2 * LOADS>();
-        else if (n_tiles > 1)
-            wait_loads<LOADS>();
-        else
-            wait_loads<0>();
-        lds_barrier();
+        if constexpr (SPLIT == 1) {
+            if (n_tiles > 2)
+                wait_loads<2 * LOADS>();
+            else if (n_tiles > 1)
+                wait_loads<LOADS>();
+            else
+                wait_loads<0>();
+            lds_barrier();
+        }
         if (!live) {
             // No query rows for this wave: it only loads.
             for (uint32_t t = 0; t < n_tiles; ++t) {
                 enter(t);
-                issue(t + 3);
-                if constexpr (PAGE8)
-                    next_id = id_at(entry_of(t + 4));
+                if (SPLIT == 1 || t > 0)
+                    issue(t + AHEAD);
+                if (SPLIT == 2)
+                    clear_nonfinite(t);
+                if constexpr (PAGE8) {
+                    locate_next(t);
+                    next_ids();
+                }
+            }
+            if constexpr (SPLIT == 2) {   // as the waves that join their results
+                lds_barrier();
+                lds_barrier();
             }
             continue;
         }
@@ -765,7 +855,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         uint64_t lagging;
         // Masks the scores of tile t if they have to be, and moves the reference if it lags.
         auto settle = [&](uint32_t t) __attribute__((always_inline)) {
-            const uint32_t p0 = (tile0 + t) * TILE;
+            const uint32_t p0 = tile_start(t);
             if (p0 + TILE > cached) {
                 const uint32_t seen = seen_rows(p0);
                 mx = -INFINITY;
@@ -790,19 +880,37 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                         scale_sum(o[i], e, keep);
             }
         };
-        {
-            s = scores(0, [](auto) {});
+        auto maximum = [&]() __attribute__((always_inline)) {
             mx = s[0];
 #pragma unroll
             for (int i = 1; i < 16; ++i)
                 mx = fmaxf(mx, s[i]);
             mx = fmaxf(mx, swap32(mx)) * c;
             lagging = __ballot(mx > mref + kSlack);
+        };
+        if constexpr (SPLIT == 1) {
+            s = scores(0, [](auto) {});
+            maximum();
             settle(0);
         }
 
         for (uint32_t t = 0; t < n_tiles; ++t) {
             enter(t);
+            if constexpr (SPLIT == 2) {
+                // The loads of step t + 1 are spread over the products.
+                s = scores(t, [&](auto index) __attribute__((always_inline)) {
+                    constexpr int k = index, i = k / 16, g = k % 16 / 4;
+                    if constexpr (k >= 0 && k % 16 == 0 && i < SPLIT) {
+                        locate(t + 1, i);
+                        src_on &= (uint32_t)((int32_t)(0u - t) >> 31);   // step 0: they are on their way
+                    }
+                    if constexpr (k >= 0 && k % 4 == 3 && i < SPLIT && g < GROUPS)
+                        load(std::integral_constant<int, g>{}, i);
+                });
+                maximum();
+                settle(t);
+                clear_nonfinite(t);
+            }
             const char* st = smem + stage_of(t);
             const uint32_t v_at = FP8 ? stage_of(t) + v_off8() : 0;
             auto vfrag = [&](int v) __attribute__((always_inline)) -> Frag {
@@ -833,21 +941,28 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     pk[k] = pack_bf16x2(e0, e1);
                 }
             };
-            const f32x16 next_s = scores(t + 1, [&](auto index) __attribute__((always_inline)) {
-                constexpr int k = index;
-                if constexpr (k < 0) {
-                    weights(0);
-                    weights(1);
-                } else if constexpr (FP8 ? k < 6 : k % 3 == 0 && k / 3 < 6) {
-                    weights(2 + (FP8 ? k : k / 3));
-                }
-                if constexpr (k == 4)
-                    locate(t + 3);
-                if constexpr (k >= KN - VD)
-                    vf[k - (KN - VD)] = vfrag(k - (KN - VD));
-            });
+            if constexpr (SPLIT == 1) {
+                const f32x16 next_s = scores(t + 1, [&](auto index) __attribute__((always_inline)) {
+                    constexpr int k = index;
+                    if constexpr (k < 0) {
+                        weights(0);
+                        weights(1);
+                    } else if constexpr (FP8 ? k < 6 : k % 3 == 0 && k / 3 < 6) {
+                        weights(2 + (FP8 ? k : k / 3));
+                    }
+                    if constexpr (k == 4)
+                        locate(t + AHEAD, 0);
+                    if constexpr (k >= KN - VD)
+                        vf[k - (KN - VD)] = vfrag(k - (KN - VD));
+                });
+                s = next_s;
+            } else {
+#pragma unroll
+                for (int v = 0; v < VD; ++v)
+                    vf[v] = vfrag(v);
+                each<8>([&](auto k) __attribute__((always_inline)) { weights(k); });
+            }
             l += sum;
-            s = next_s;
             // e4m3: the weights times the scales of one block of 128 features at a time, rounded
             // to bf16 once.
             bf16x8 pf[2];
@@ -873,16 +988,18 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of_codes(vf[v % VD]), pf[v & 1], o[v >> 1], 0, 0, 0);
                 if constexpr (v + VD < VN)
                     vf[v % VD] = vfrag(v + VD);
-                if constexpr (v % 8 == 3 && v / 8 < GROUPS)
-                    load(std::integral_constant<int, v / 8>{});
-                if constexpr (v >= 4 && v < 20 && v % 2 == 0)
-                    mx = v == 4 ? fmaxf(s[0], s[1]) : fmaxf(fmaxf(mx, s[v - 4]), s[v - 3]);
-                if constexpr (v == 20)
-                    mx = fmaxf(mx, swap32(mx)) * c;
-                if constexpr (v == 22)
-                    lagging = __ballot(mx > mref + kSlack);
+                if constexpr (SPLIT == 1) {
+                    if constexpr (v % 8 == 3 && v / 8 < GROUPS)
+                        load(std::integral_constant<int, v / 8>{}, 0);
+                    if constexpr (v >= 4 && v < 20 && v % 2 == 0)
+                        mx = v == 4 ? fmaxf(s[0], s[1]) : fmaxf(fmaxf(mx, s[v - 4]), s[v - 3]);
+                    if constexpr (v == 20)
+                        mx = fmaxf(mx, swap32(mx)) * c;
+                    if constexpr (v == 22)
+                        lagging = __ballot(mx > mref + kSlack);
+                }
                 if constexpr (PAGE8 && v == 24)
-                    next_entry = entry_of(t + 4);
+                    locate_next(t);
                 if constexpr (FP8) {
                     // The next block's weights, a quarter at a time.
                     constexpr int b = (v >> 3) + 1, at = v & 7;
@@ -894,32 +1011,56 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 __builtin_amdgcn_sched_barrier(0);
             });
             if constexpr (PAGE8)
-                next_id = id_at(next_entry);
-            if (t + 1 < n_tiles)
+                next_ids();
+            if (SPLIT == 1 && t + 1 < n_tiles)
                 settle(t + 1);
         }
 
         l += swap32(l);
-        if (tile0 == 0 && tile1 + ITEM_COST == r.nu) {
-            const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-            store_row(static_cast<uint16_t*>(a.out) + (int64_t)qrow * K, o, inv, valid, half);
-            if (a.lse && valid && half == 0)
-                a.lse[qrow] = l == 0.0f ? -INFINITY : mref * kLn2 + __logf(l);
+        const bool whole = tile0 == 0 && tile1 + COST == r.nu;
+        float* piece = a.ws + (size_t)(2 * w + (tile0 == 0 ? 1 : 0)) * P.piece + (size_t)qwave * PIECE_WAVE;
+        if constexpr (SPLIT == 1) {
+            store_result<0, 16>(a, o, mref, l, qrow, valid, whole, piece, lane);
         } else {
-            // A share of the item: sums, maximum and sum as they are, in lane order.
-            float* piece = a.ws + (size_t)(2 * w + (tile0 == 0 ? 1 : 0)) * P.piece + (size_t)wave * PIECE_WAVE;
-#pragma unroll
-            for (int fb = 0; fb < 16; ++fb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    *reinterpret_cast<f32x4*>(piece + ((fb * 4 + i) * 64 + lane) * 4) =
+            // The two waves of the same rows join their results: each hands the other half of its
+            // sums through LDS, and keeps the half it stores.
+            constexpr int WAVE_BYTES = 8 * 16 * 256 + 256;
+            static_assert(WAVES * WAVE_BYTES <= sizeof(smem), "LDS");
+            auto join = [&](auto first) __attribute__((always_inline)) {
+                constexpr int keep = first, give = 8 - keep;
+                char* mine = smem + wave * WAVE_BYTES;
+                const char* other = smem + (wave ^ 2) * WAVE_BYTES;
+                lds_barrier();   // the stages are no longer read
+                each<32>([&](auto index) __attribute__((always_inline)) {
+                    constexpr int q = index, fb = give + q / 4, i = q % 4;
+                    *reinterpret_cast<f32x4*>(mine + (q * 64 + lane) * 16) =
                         f32x4{o[fb][4 * i], o[fb][4 * i + 1], o[fb][4 * i + 2], o[fb][4 * i + 3]};
                     __builtin_amdgcn_sched_barrier(0);
-                }
-            if (half == 0) {
-                piece[32 * K + col] = mref;
-                piece[32 * K + 32 + col] = l;
-            }
+                });
+                reinterpret_cast<float*>(mine + 8 * 16 * 256)[lane] = half ? l : mref;
+                lds_barrier();
+                const float* ml = reinterpret_cast<const float*>(other + 8 * 16 * 256);
+                const float m2 = ml[col], l2 = ml[32 + col];
+                const float next = fmaxf(mref, m2);
+                const float at = next == -INFINITY ? 0.0f : next;
+                const float f1 = __builtin_amdgcn_exp2f(mref - at), f2 = __builtin_amdgcn_exp2f(m2 - at);
+                l = l * f1 + l2 * f2;
+                mref = next;
+                each<32>([&](auto index) __attribute__((always_inline)) {
+                    constexpr int q = index, fb = keep + q / 4, i = q % 4;
+                    const f32x4 y = *reinterpret_cast<const f32x4*>(other + (q * 64 + lane) * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[fb][4 * i + e] = o[fb][4 * i + e] * f1 + y[e] * f2;
+                    if constexpr (q % 4 == 3)
+                        __builtin_amdgcn_sched_barrier(0);
+                });
+                store_result<keep, 8>(a, o, mref, l, qrow, valid, whole, piece, lane);
+            };
+            if (pair == 0)
+                join(std::integral_constant<int, 0>{});
+            else
+                join(std::integral_constant<int, 8>{});
         }
     }
 }
@@ -934,8 +1075,8 @@ __global__ void __launch_bounds__(256) tree_attention_join(MfmaParams P)
     __shared__ float top[8][32];
     __shared__ f32x4 part[3][2][64];
     const TreeAttentionArgs& a = P.a;
-    const uint32_t g = blockIdx.x & 3;
-    const auto* words = (const __attribute__((address_space(4))) uint32_t*)(uint64_t)(P.cuts + (blockIdx.x >> 2));
+    const uint32_t g = blockIdx.x & (P.groups - 1);
+    const auto* words = (const __attribute__((address_space(4))) uint32_t*)(uint64_t)(P.cuts + blockIdx.x / P.groups);
     const Cut rec{words[0], words[1], words[2], words[3], words[4], {}};
     if (rec.rows <= g * 32)
         return;
@@ -1104,7 +1245,7 @@ bool tree_attention_mfma_fits(const TreeAttentionArgs& a, AttnKind kind)
            (kind == ATTN_BF16 || a.Ls.stride_token < (int64_t(1) << 28)) &&
            (uint64_t)a.L.batch * a.L.max_pages < (uint64_t(1) << 32) &&
            // items (at most one partly filled per request) times units
-           ((uint64_t)a.T * a.H / kAttnRows + std::min<uint64_t>(a.L.batch, a.T)) * (a.capacity / TILE + 1 + ITEM_COST) <
+           ((uint64_t)a.T * a.H / Shape<2>::ROWS + std::min<uint64_t>(a.L.batch, a.T)) * (a.capacity / TILE + 1 + Shape<1>::COST) <
                (uint64_t(1) << 31);
 }
 
@@ -1122,20 +1263,32 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind,
         P.ps_magic = (uint32_t)(((uint64_t(1) << (31 + sh)) + ps - 1) / ps);
         P.ps_shift = sh - 1;
     }
-    const int64_t waves = (std::min<int64_t>((int64_t)a.T * a.H, kAttnRows) + 31) / 32;
+    // Two pairs of waves where an average request fills no more than half of a wide item.  Wide /
+    // two pairs, us: 16 requests x 16 heads x 3-4 tokens, 20-40 thousand rows: e4m3 190 / 133, bf16
+    // 148 / 146; 64 x 16 heads, 256-4096 rows: e4m3 67 / 50, bf16 53 / 43.  Above, they are slower:
+    // 16 x 16 heads x 5-6 tokens: e4m3 194 / 211, bf16 162 / 206 (each item reads all of its rows);
+    // 64 x 128 heads, bf16: 70 / 75.
+    const bool split = (int64_t)a.T * a.H <= (int64_t)Shape<2>::ROWS * a.L.batch;
+    P.groups = split ? 2 : 4;
+    const int64_t waves = (std::min<int64_t>((int64_t)a.T * a.H, (int64_t)P.groups * 32) + 31) / 32;
     P.piece = (uint32_t)(waves * PIECE_WAVE);
-    P.min_tiles = 4;
+    P.min_tiles = split ? 2 : 4;   // steps: 4 tiles either way
     P.cuts = reinterpret_cast<Cut*>(a.ws + (size_t)2 * kAttnGroups * P.piece);
-    const bool fp8 = kind == ATTN_E4M3;
+    const bool fp8 = kind == ATTN_E4M3, page8 = ps % 8 == 0;
     log_launch(fp8 ? "tree_attention_mfma<e4m3>" : "tree_attention_mfma<bf16>", kAttnGroups, 64 * WAVES,
-               "T=%d H=%d page_size=%u", a.T, a.H, ps);
-    auto* kernel = fp8 ? (ps % 8 == 0 ? tree_attention_mfma<true, true> : tree_attention_mfma<false, true>)
-                       : (ps % 8 == 0 ? tree_attention_mfma<true, false> : tree_attention_mfma<false, false>);
+               "T=%d H=%d page_size=%u rows=%u", a.T, a.H, ps, P.groups * 32);
+    auto pick = [&](auto page, auto cache) {
+        constexpr bool p = decltype(page)::value, e = decltype(cache)::value;
+        return split ? tree_attention_mfma<p, e, 2> : tree_attention_mfma<p, e, 1>;
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    auto* kernel = fp8 ? (page8 ? pick(yes, yes) : pick(no, yes)) : (page8 ? pick(yes, no) : pick(no, no));
     hipLaunchKernelGGL(kernel, dim3(kAttnGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
     // One block per cut and 32 rows of an item.
-    const unsigned join_blocks = kAttnGroups * 4;
+    const unsigned join_blocks = kAttnGroups * P.groups;
     log_launch("tree_attention_join", join_blocks, 256, "T=%d H=%d", a.T, a.H);
     hipLaunchKernelGGL(tree_attention_join, dim3(join_blocks), dim3(256), 0, s, P);
     return hipGetLastError();
