@@ -594,14 +594,14 @@ typedef struct {
  *     pair(b) = d_rope * ln(original_max_position / (2 pi b)) / (2 ln theta)
  *   (the by-parts interpolation published as YaRN, Peng et al. 2023).
  *
- * The frequencies and each angle's reduction to a quarter turn are in binary64, the
- * sine and cosine of the reduced angle in binary32.
+ * All of it is in binary64, up to the one rounding to float.
  *
  * params          [host]
  * first_position  >= 0; first_position + rows <= 2^31
  * d_rope          even, 2 <= d_rope <= 512
  * freqs_cis       [device] float [rows][d_rope], 8-byte aligned, written
- * Parameters that are not finite or out of the ranges above: MLA_ERR_INVALID_SHAPE.
+ * Parameters that are not finite or out of the ranges above, and frequencies that reach
+ * angles of 2^50 quarter turns within the rows: MLA_ERR_INVALID_SHAPE.
  */
 mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t first_position, int32_t rows,
                             int32_t d_rope, float* freqs_cis, void* stream);

@@ -57,13 +57,11 @@ MLA_API mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t fir
         return MLA_ERR_MISALIGNED;
     if (rows == 0)
         return MLA_OK;
-    if (mla_status_t st = check_device())
-        return st;
 
     constexpr double kPi = 3.14159265358979323846;
     RopeFreqsArgs a{};
     a.out = freqs_cis;
-    a.amplitude = (float)p.amplitude;
+    a.amplitude = p.amplitude;
     a.first = first_position;
     a.rows = rows;
     a.pairs = d_rope / 2;
@@ -84,7 +82,12 @@ MLA_API mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t fir
             f = f / p.factor * r + f * (1 - r);
         }
         a.quarters[j] = f / (kPi / 2);
+        // No angle of 2^50 quarter turns: two bits of it would be left.
+        if (!(a.quarters[j] * ((double)first_position + rows) < 0x1p50))
+            return MLA_ERR_INVALID_SHAPE;
     }
+    if (mla_status_t st = check_device())
+        return st;
     const hipError_t e = launch_rope_freqs(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MLA_OK : hip_failed(e);
 }

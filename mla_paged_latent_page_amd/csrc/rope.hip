@@ -3,11 +3,11 @@
 //
 // rope_freqs_kernel: entry (p, j) is (cos, sin) of p * g_j.  A position of 10^6
 // times a frequency of 1 has 20 bits before the binary point, so binary32 would
-// leave four for the angle: the product with g_j in quarter turns and its
-// reduction to [-1/2, 1/2] quarter turns are binary64 (three operations), and
-// only the reduced angle is rounded to binary32 (2^-26 quarter turns) for the
-// Taylor sums of sine and cosine, which stop below 2^-25 at pi/4.  Bound by its
-// stores.
+// leave four for the angle: the product with g_j in quarter turns, its reduction
+// to [-1/2, 1/2] quarter turns and the Taylor sums of sine and cosine, which stop
+// below 2^-30 at pi/4, are binary64, and the result, times the amplitude, is rounded
+// once.  Bound by its stores all the same; a thread divides once,
+// then walks rows and pairs by the grid's step.
 //
 // rope_q_kernel: one block per token (and 64 heads).  A thread keeps one group of
 // pairs of the rope part for every head it visits, so the token's (cos, sin) row is
@@ -20,25 +20,37 @@
 namespace mla {
 namespace {
 
-__global__ void __launch_bounds__(256) rope_freqs_kernel(RopeFreqsArgs a)
+__global__ void __launch_bounds__(256) rope_freqs_kernel(RopeFreqsArgs a, int step_rows, int step_pairs)
 {
     const int64_t total = (int64_t)a.rows * a.pairs;
-    const int64_t step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
-        const int row = (int)(i / a.pairs);
-        const int j = (int)(i - (int64_t)row * a.pairs);
-        const double turn = (double)((int64_t)a.first + row) * a.quarters[j];
-        const double n = rint(turn);
-        const float x = (float)(turn - n) * 1.57079632679489662f;
-        const int quadrant = (int)((int64_t)n & 3);
-        const float x2 = x * x;
-        const float sx = x + x * x2 * (-1.0f / 6 + x2 * (1.0f / 120 + x2 * (-1.0f / 5040 + x2 * (1.0f / 362880))));
-        const float cx = 1.0f + x2 * (-0.5f + x2 * (1.0f / 24 + x2 * (-1.0f / 720 + x2 * (1.0f / 40320 -
-                         x2 * (1.0f / 3628800)))));
-        const float s1 = (quadrant & 1) ? cx : sx, c1 = (quadrant & 1) ? sx : cx;
-        const float s = (quadrant & 2) ? -s1 : s1;
-        const float c = (quadrant == 1 || quadrant == 2) ? -c1 : c1;
-        *reinterpret_cast<f32x2*>(a.out + 2 * i) = f32x2{c * a.amplitude, s * a.amplitude};
+    const int64_t step = (int64_t)gridDim.x * 256;   // step_rows rows and step_pairs pairs
+    const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    int row = (int)(first / a.pairs);
+    int j = (int)(first - (int64_t)row * a.pairs);
+    double quarters = first < total ? a.quarters[j] : 0.0;
+    for (int64_t i = first; i < total; i += step) {
+        const double turn = (double)((uint32_t)a.first + (uint32_t)row) * quarters;
+        // Rounded to an integer by a sum whose last place is 1, where its low bits are too.
+        constexpr double kWhole = 0x1.8p52;
+        const double whole = turn + kWhole;
+        const uint32_t quadrant = (uint32_t)__builtin_bit_cast(uint64_t, whole);
+        const double x = (turn - (whole - kWhole)) * 1.57079632679489661923, x2 = x * x;
+        const double sx = x + x * x2 * (-1.0 / 6 + x2 * (1.0 / 120 + x2 * (-1.0 / 5040 + x2 * (1.0 / 362880 -
+                          x2 * (1.0 / 39916800)))));
+        const double cx = 1.0 + x2 * (-0.5 + x2 * (1.0 / 24 + x2 * (-1.0 / 720 + x2 * (1.0 / 40320 -
+                          x2 * (1.0 / 3628800)))));
+        const float sa = (float)(sx * a.amplitude), ca = (float)(cx * a.amplitude);
+        const float s = (quadrant & 1) ? ca : sa, c = (quadrant & 1) ? sa : ca;
+        const uint32_t s_sign = quadrant << 30 & 0x80000000u, c_sign = (quadrant + 1) << 30 & 0x80000000u;
+        *reinterpret_cast<f32x2*>(a.out + 2 * i) = f32x2{__uint_as_float(__float_as_uint(c) ^ c_sign),
+                                                         __uint_as_float(__float_as_uint(s) ^ s_sign)};
+        row += step_rows;
+        if (step_pairs) {
+            j += step_pairs;
+            if (j >= a.pairs)
+                j -= a.pairs, ++row;
+            quarters = a.quarters[j];
+        }
     }
 }
 
@@ -173,7 +185,8 @@ hipError_t launch_rope_freqs(const RopeFreqsArgs& a, hipStream_t s)
     const int64_t total = (int64_t)a.rows * a.pairs;
     const unsigned grid = (unsigned)std::min<int64_t>((total + 255) / 256, 256 * 16);
     log_launch("rope_freqs_kernel", grid, 256, "rows=%d pairs=%d", a.rows, a.pairs);
-    hipLaunchKernelGGL(rope_freqs_kernel, dim3(grid), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(rope_freqs_kernel, dim3(grid), dim3(256), 0, s, a, (int)((int64_t)grid * 256 / a.pairs),
+                       (int)((int64_t)grid * 256 % a.pairs));
     return hipGetLastError();
 }
 

@@ -12,7 +12,7 @@ constexpr int kMaxRopePairs = 256;
 struct RopeFreqsArgs {
     double quarters[kMaxRopePairs];   // quarter turns per position of each pair
     float* out;                       // [rows][2 * pairs]
-    float amplitude;
+    double amplitude;
     int first, rows, pairs;
 };
 

@@ -38,11 +38,9 @@ def test_rope_freqs(first, rows, dim, scaling, factor, amplitude):
     f = frequencies(dim, 10000.0, scaling, factor, 4096)
     ang = (first + np.arange(rows, dtype=np.float64))[:, None] * f
     ref = np.stack([np.cos(ang), np.sin(ang)], 2).reshape(rows, dim) * amplitude
-    # The reduced angle is rounded to 2^-26 quarter turns and scaled by pi/2 (0.9 x 2^-24),
-    # the sums of sine and cosine round by at most 1.6 x 2^-24, the amplitude and its
-    # product by 2^-24; and a binary64 angle of a turns is off by a 2^-52 turns, twice
-    # (the table's and the reference's).
-    tol = amplitude * (4 * U32 + 4 * np.repeat(np.abs(ang), 2, axis=1) * 2.0 ** -52)
+    # One rounding (at most 2^-24 of the amplitude), and a binary64 angle of a turns is off by
+    # a 2^-52 turns, twice (the table's and the reference's).
+    tol = amplitude * (U32 + 4 * np.repeat(np.abs(ang), 2, axis=1) * 2.0 ** -52)
     assert np.all(np.abs(out.double().cpu().numpy() - ref) <= tol)
 
 

@@ -61,6 +61,13 @@ def test_rope_freqs_refusals(lib):
     assert freqs(lib) == DEV and freqs(lib, scaling=2, orig=4096, factor=4.0) == DEV
 
 
+def test_rope_freqs_refuses_angles_beyond_binary64(lib):
+    # 2^50 quarter turns are 1.77e15 rad.
+    assert freqs(lib, theta=1e-300) == SHAPE and freqs(lib, scaling=1, factor=1e-320) == SHAPE
+    assert freqs(lib, scaling=1, factor=1e-9, first=10 ** 7) == SHAPE
+    assert freqs(lib, scaling=1, factor=1e-9, first=10 ** 6) == DEV
+
+
 def rope_q(lib, q=FAKE, st=16 * 192, sh=192, T=5, H=16, nope=128, R=64, dt=1, pos=FAKE, fr=FAKE, ms=100, lay=0, out=FAKE,
            ost=None, osh=None):
     return lib.mla_rope_q(q, st, sh, T, H, nope, R, dt, pos, fr, ms, lay, out, st if ost is None else ost,
