@@ -247,10 +247,10 @@ class PagedKVCache:
 def _stream(stream):
     import torch
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     # torch.cuda.current_stream() without the Stream object around the handle: it costs more
     # than a small call's kernel.
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _nbytes(t):
@@ -280,18 +280,23 @@ def _u32(t, what, entries=0):
     return t.data_ptr()
 
 
-def _gpu(**tensors):
-    """Every tensor a call hands to the library must live on the current GPU; anything
-    else (a host tensor, another GPU's tensor) is refused before any launch."""
+def _gpu(cache=None, **tensors):
+    """Every tensor a call hands to the library (the cache's too) must live on the current GPU;
+    anything else (a host tensor, another GPU's tensor) is refused before any launch."""
     import torch
+    items = tensors.items()
+    if cache is not None:
+        items = (*items, ("cache.pool", cache.pool), ("cache.page_table", cache.page_table),
+                 ("cache.cache_lengths", cache.cache_lengths), ("cache.scales", cache.scales))
     current = None
-    for name, t in tensors.items():
+    for name, t in items:
         if t is None:
             continue
-        if isinstance(t, torch.Tensor) and t.is_cuda:
+        device = t.get_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+        if device >= 0:
             if current is None:
-                current = torch.cuda.current_device()
-            if t.get_device() == current:
+                current = torch._C._cuda_getDevice()
+            if device == current:
                 continue
         raise ValueError(f"{name} must be a tensor on the current GPU")
 
@@ -318,11 +323,6 @@ def _cache_desc(cache, scales=False):
     if not scales:
         return desc
     return desc, cache.scales_descriptor()
-
-
-def _cache_tensors(cache):
-    return {"cache.pool": cache.pool, "cache.page_table": cache.page_table,
-            "cache.cache_lengths": cache.cache_lengths, "cache.scales": cache.scales}
 
 
 def _index_args(buffer_row_offsets, cache_offsets, desc):
@@ -374,7 +374,7 @@ def mla_decompress_k_paged(buffer_row_offsets, cache_offsets, buffer_length: int
     lat, out = _check_outputs(buffer_length, desc, N, k_latent_buffer, k_buffer)
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, weight=weight,
-         k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, **_cache_tensors(cache))
+         k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, cache=cache)
     st = lib().mla_decompress_k_paged(bro, co, int(buffer_length), w, N, K, ctypes.byref(desc), int(layer_idx),
                                       lat, out, _stream(stream))
     _check(st, "mla_decompress_k_paged")
@@ -389,7 +389,7 @@ def mla_gather_latent_paged(buffer_row_offsets, cache_offsets, buffer_length: in
                _dtypes().get(desc.dtype))
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, k_latent_buffer=k_latent_buffer,
-         **_cache_tensors(cache))
+         cache=cache)
     st = lib().mla_gather_latent_paged(bro, co, int(buffer_length), ctypes.byref(desc), int(layer_idx), lat,
                                        _stream(stream))
     _check(st, "mla_gather_latent_paged")
@@ -420,7 +420,7 @@ def mla_check_indices(row_offsets, cache_offsets, rows: int, cache: PagedKVCache
     (status, first failing request or -1); never raises on a failed check."""
     desc = _cache_desc(cache)
     bad = ctypes.c_int64(-1)
-    _gpu(row_offsets=row_offsets, cache_offsets=cache_offsets, **_cache_tensors(cache))
+    _gpu(row_offsets=row_offsets, cache_offsets=cache_offsets, cache=cache)
     st = lib().mla_check_indices(_u32(row_offsets, "row_offsets", desc.batch_size + 1),
                                  _u32(cache_offsets, "cache_offsets", desc.batch_size)
                                  if cache_offsets is not None else None,
@@ -461,7 +461,7 @@ def mla_decompress_k_paged_fp8(buffer_row_offsets, cache_offsets, buffer_length:
     ws, ws_bytes = _workspace(workspace)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, weight_e4m3=weight_e4m3,
          weight_scale=weight_scale, k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, workspace=workspace,
-         **_cache_tensors(cache))
+         cache=cache)
     st = lib().mla_decompress_k_paged_fp8(bro, co, int(buffer_length), w, sw, N, K, m_gran, n_gran, k_gran,
                                           ctypes.byref(desc), int(layer_idx), lat, out, ws, ws_bytes,
                                           _stream(stream))
@@ -482,7 +482,7 @@ def mla_decompress_k_paged_fp8_noalloc(buffer_row_offsets, cache_offsets, buffer
     lat, out = _check_outputs(buffer_length, desc, N, k_latent_buffer, k_buffer, (torch.bfloat16,))
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, weight_e4m3=weight_e4m3,
-         weight_scale=weight_scale, k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, **_cache_tensors(cache))
+         weight_scale=weight_scale, k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, cache=cache)
     st = lib().mla_decompress_k_paged_fp8_noalloc(bro, co, int(buffer_length), w, sw, N, K, m_gran, n_gran,
                                                   k_gran, ctypes.byref(desc), int(layer_idx), lat, out,
                                                   _stream(stream))
@@ -503,7 +503,7 @@ def mla_decompress_kv_paged(buffer_row_offsets, cache_offsets, buffer_length: in
     vout = _buf(v_buffer, "v_buffer", buffer_length * N_v * _bytes_of(desc.dtype), dt)
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, w_k=w_k, w_v=w_v,
-         k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, v_buffer=v_buffer, **_cache_tensors(cache))
+         k_latent_buffer=k_latent_buffer, k_buffer=k_buffer, v_buffer=v_buffer, cache=cache)
     st = lib().mla_decompress_kv_paged(bro, co, int(buffer_length), wk, N_k, wv, N_v, K, ctypes.byref(desc),
                                        int(layer_idx), lat, kout, vout, _stream(stream))
     _check(st, "mla_decompress_kv_paged")
@@ -529,7 +529,7 @@ def mla_decompress_kv_paged_fp8(buffer_row_offsets, cache_offsets, buffer_length
     ws, ws_bytes = _workspace(workspace)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, w_k_e4m3=w_k_e4m3,
          w_k_scale=w_k_scale, w_v_e4m3=w_v_e4m3, w_v_scale=w_v_scale, k_latent_buffer=k_latent_buffer,
-         k_buffer=k_buffer, v_buffer=v_buffer, workspace=workspace, **_cache_tensors(cache))
+         k_buffer=k_buffer, v_buffer=v_buffer, workspace=workspace, cache=cache)
     st = lib().mla_decompress_kv_paged_fp8(bro, co, int(buffer_length), wk, sk, N_k, wv, sv, N_v, K,
                                            m_gran, n_gran, k_gran, ctypes.byref(desc), int(layer_idx),
                                            lat, kout, vout, ws, ws_bytes, _stream(stream))
@@ -559,7 +559,7 @@ def mla_decompress_k_paged_fp8_cache(buffer_row_offsets, cache_offsets, buffer_l
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, w_k_e4m3=w_k_e4m3,
          w_k_scale=w_k_scale, k_latent_buffer=k_latent_buffer, k_latent_scales=k_latent_scales,
-         k_buffer=k_buffer, **_cache_tensors(cache))
+         k_buffer=k_buffer, cache=cache)
     st = lib().mla_decompress_k_paged_fp8_cache(bro, co, int(buffer_length), w, sw, N, K, ctypes.byref(desc),
                                                 ctypes.byref(sdesc), int(layer_idx), lat, lsc, out,
                                                 _stream(stream))
@@ -586,7 +586,7 @@ def mla_decompress_kv_paged_fp8_cache(buffer_row_offsets, cache_offsets, buffer_
     bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
     _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, w_k_e4m3=w_k_e4m3,
          w_k_scale=w_k_scale, w_v_e4m3=w_v_e4m3, w_v_scale=w_v_scale, k_latent_buffer=k_latent_buffer,
-         k_latent_scales=k_latent_scales, k_buffer=k_buffer, v_buffer=v_buffer, **_cache_tensors(cache))
+         k_latent_scales=k_latent_scales, k_buffer=k_buffer, v_buffer=v_buffer, cache=cache)
     st = lib().mla_decompress_kv_paged_fp8_cache(bro, co, int(buffer_length), wk, sk, N, wv, sv, Nv, K,
                                                  ctypes.byref(desc), ctypes.byref(sdesc), int(layer_idx),
                                                  lat, lsc, kout, vout, _stream(stream))
@@ -664,7 +664,7 @@ def mla_write_latent_paged(kv_input, input_row_offsets, kv_norm_gamma, epsilon: 
     desc = _cache_desc(cache)
     T, x, iro, g, fr, max_seq = _latent_write_args(kv_input, input_row_offsets, kv_norm_gamma, freqs_cis, K, desc)
     _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, kv_norm_gamma=kv_norm_gamma,
-         freqs_cis=freqs_cis, **_cache_tensors(cache))
+         freqs_cis=freqs_cis, cache=cache)
     st = lib().mla_write_latent_paged(x, iro, T, g, float(epsilon), fr, int(max_seq), int(K), ctypes.byref(desc),
                                       int(layer_idx), _stream(stream))
     _check(st, "mla_write_latent_paged")
@@ -677,7 +677,7 @@ def mla_write_latent_paged_fp8(kv_input, input_row_offsets, kv_norm_gamma, epsil
     desc, sdesc = _cache_desc(cache, scales=True)
     T, x, iro, g, fr, max_seq = _latent_write_args(kv_input, input_row_offsets, kv_norm_gamma, freqs_cis, K, desc)
     _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, kv_norm_gamma=kv_norm_gamma,
-         freqs_cis=freqs_cis, **_cache_tensors(cache))
+         freqs_cis=freqs_cis, cache=cache)
     st = lib().mla_write_latent_paged_fp8(x, iro, T, g, float(epsilon), fr, int(max_seq), int(K),
                                           ctypes.byref(desc), ctypes.byref(sdesc), int(layer_idx), _stream(stream))
     _check(st, "mla_write_latent_paged_fp8")
@@ -699,7 +699,7 @@ def kv_matmul_paged(hidden_state, input_row_offsets, weight, cache: PagedKVCache
     if input_row_offsets.numel() != desc.batch_size + 1:
         raise ValueError("input_row_offsets must have batch_size + 1 entries")
     iro = _u32(input_row_offsets, "input_row_offsets", desc.batch_size + 1)
-    _gpu(hidden_state=hidden_state, input_row_offsets=input_row_offsets, weight=weight, **_cache_tensors(cache))
+    _gpu(hidden_state=hidden_state, input_row_offsets=input_row_offsets, weight=weight, cache=cache)
     st = lib().kv_matmul_paged(h, iro, T, Kd, w, ctypes.byref(desc), int(layer_idx), _stream(stream))
     _check(st, "kv_matmul_paged")
 
@@ -773,7 +773,7 @@ def mla_write_latent_paged_at(kv_input, input_row_offsets, positions, kv_norm_ga
     pos = _u32(positions, "positions", T)
     lay = _rope_layout(layout)
     _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, positions=positions, kv_norm_gamma=kv_norm_gamma,
-         freqs_cis=freqs_cis, **_cache_tensors(cache))
+         freqs_cis=freqs_cis, cache=cache)
     st = lib().mla_write_latent_paged_at(x, iro, T, pos, g, float(epsilon), fr, int(max_seq), int(K), lay,
                                          ctypes.byref(desc), int(layer_idx), _stream(stream))
     _check(st, "mla_write_latent_paged_at")
@@ -788,7 +788,7 @@ def mla_write_latent_paged_fp8_at(kv_input, input_row_offsets, positions, kv_nor
     pos = _u32(positions, "positions", T)
     lay = _rope_layout(layout)
     _gpu(kv_input=kv_input, input_row_offsets=input_row_offsets, positions=positions, kv_norm_gamma=kv_norm_gamma,
-         freqs_cis=freqs_cis, **_cache_tensors(cache))
+         freqs_cis=freqs_cis, cache=cache)
     st = lib().mla_write_latent_paged_fp8_at(x, iro, T, pos, g, float(epsilon), fr, int(max_seq), int(K), lay,
                                              ctypes.byref(desc), ctypes.byref(sdesc), int(layer_idx),
                                              _stream(stream))
@@ -839,7 +839,7 @@ def mla_tree_attention_paged(q_latent, input_row_offsets, tree_mask, scale: floa
                                                          lse, dtype)
     ws, ws_bytes = _workspace(workspace)
     _gpu(q_latent=q_latent, input_row_offsets=input_row_offsets, tree_mask=tree_mask, out_latent=out_latent, lse=lse,
-         workspace=workspace, **_cache_tensors(cache))
+         workspace=workspace, cache=cache)
     st = lib().mla_tree_attention_paged(q, iro, T, H, mask, words, float(scale), int(K), ctypes.byref(desc),
                                         int(layer_idx), out, ls, ws, ws_bytes, _stream(stream))
     _check(st, "mla_tree_attention_paged")
@@ -855,7 +855,7 @@ def mla_tree_attention_paged_fp8_cache(q_latent, input_row_offsets, tree_mask, s
                                                          lse, torch.bfloat16)
     ws, ws_bytes = _workspace(workspace)
     _gpu(q_latent=q_latent, input_row_offsets=input_row_offsets, tree_mask=tree_mask, out_latent=out_latent, lse=lse,
-         workspace=workspace, **_cache_tensors(cache))
+         workspace=workspace, cache=cache)
     st = lib().mla_tree_attention_paged_fp8_cache(q, iro, T, H, mask, words, float(scale), int(K), ctypes.byref(desc),
                                                   ctypes.byref(sdesc), int(layer_idx), out, ls, ws, ws_bytes,
                                                   _stream(stream))
@@ -877,7 +877,7 @@ def mla_copy_pages(src_pages, dst_pages, cache: PagedKVCache, stream=None) -> No
     if dst_pages.numel() != n:
         raise ValueError("src_pages and dst_pages must have the same number of entries")
     src, dst = _u32(src_pages, "src_pages"), _u32(dst_pages, "dst_pages")
-    _gpu(src_pages=src_pages, dst_pages=dst_pages, **_cache_tensors(cache))
+    _gpu(src_pages=src_pages, dst_pages=dst_pages, cache=cache)
     st = lib().mla_copy_pages(src, dst, n, ctypes.byref(desc), sdesc, _stream(stream))
     _check(st, "mla_copy_pages")
 
@@ -891,7 +891,7 @@ def mla_fork_paged(parents, children, new_pages, ref_counts, cache: PagedKVCache
         raise ValueError("parents, children and new_pages must have the same number of entries")
     pa, ch, pg = _u32(parents, "parents"), _u32(children, "children"), _u32(new_pages, "new_pages")
     refs = _u32(ref_counts, "ref_counts", desc.num_pages)
-    _gpu(parents=parents, children=children, new_pages=new_pages, ref_counts=ref_counts, **_cache_tensors(cache))
+    _gpu(parents=parents, children=children, new_pages=new_pages, ref_counts=ref_counts, cache=cache)
     st = lib().mla_fork_paged(pa, ch, pg, n, refs, ctypes.byref(desc), sdesc, _stream(stream))
     _check(st, "mla_fork_paged")
 
@@ -904,7 +904,7 @@ def mla_free_paged(requests, ref_counts, free_list, free_count, cache: PagedKVCa
     refs = _u32(ref_counts, "ref_counts", desc.num_pages)
     fl, fc = _u32(free_list, "free_list", desc.num_pages), _u32(free_count, "free_count", 1)
     _gpu(requests=requests, ref_counts=ref_counts, free_list=free_list, free_count=free_count,
-         **_cache_tensors(cache))
+         cache=cache)
     st = lib().mla_free_paged(req, requests.numel(), refs, fl, fc, ctypes.byref(desc), _stream(stream))
     _check(st, "mla_free_paged")
 
@@ -915,7 +915,7 @@ def mla_compact_paged(accepted, accepted_offsets, cache: PagedKVCache, stream=No
     desc, sdesc = _page_descs(cache)
     acc = _u32(accepted, "accepted")
     off = _u32(accepted_offsets, "accepted_offsets", desc.batch_size + 1)
-    _gpu(accepted=accepted, accepted_offsets=accepted_offsets, **_cache_tensors(cache))
+    _gpu(accepted=accepted, accepted_offsets=accepted_offsets, cache=cache)
     st = lib().mla_compact_paged(acc, off, accepted.numel(), ctypes.byref(desc), sdesc, _stream(stream))
     _check(st, "mla_compact_paged")
 
