@@ -111,13 +111,16 @@ __device__ inline Request uniform(Request r)
                    uniform(r.nu), uniform(r.base)};
 }
 
-__device__ inline uint32_t wave_inclusive(uint32_t v, int lane)
+// Sum over the lanes up to and including this one: within rows of 16 lanes, then a row's last
+// lane into the next row, and lane 31 into the upper half.
+__device__ inline uint32_t wave_inclusive(uint32_t v)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t up = __shfl_up(v, d);
-        v += lane >= d ? up : 0u;
-    }
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
     return v;
 }
 
@@ -143,7 +146,7 @@ struct Schedule {
         mine = Request{};
         if (b0 + lane < a.L.batch)
             mine = request_at<SPLIT>(a, b0 + lane);
-        scan = wave_inclusive(mine.nm * mine.nu, lane);
+        scan = wave_inclusive(mine.nm * mine.nu);
     }
     __device__ uint32_t loaded() const { return (uint32_t)__builtin_amdgcn_readlane((int)scan, 63); }
 
@@ -159,7 +162,7 @@ struct Schedule {
             load(0, 0);
         const uint32_t want = (total + min_tiles - 1) / min_tiles;
         groups = want < 1 ? 1u : want > kAttnGroups ? (uint32_t)kAttnGroups : want;
-        share = total / groups;
+        share = groups == kAttnGroups ? total / kAttnGroups : total / groups;
         rest = total - share * groups;
         snap = share / 32;
     }
@@ -746,6 +749,12 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             return seen & (room >= 32 ? ~0u : (1u << room) - 1);
         };
 
+        f32x16 o[16];   // cleared while the first tiles are on their way
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            o[i] = f32x16{0.f};
+            asm volatile("" : "+a"(o[i]));
+        }
         if constexpr (SPLIT == 1) {
             if (n_tiles > 2)
                 wait_loads<2 * LOADS>();
@@ -775,10 +784,6 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             continue;
         }
 
-        f32x16 o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            o[i] = f32x16{0.f};
         float mref = -INFINITY, l = 0.0f;
 
         // Scores of tile t: lane (col, half) gets rows 8 (i / 4) + 4 half + i % 4 for its query.
@@ -872,12 +877,14 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 const float keep = next == mref ? 1.0f : __builtin_amdgcn_exp2f(mref - next);
                 mref = next;
                 l *= keep;
-                asm volatile("s_nop 15");   // the last products' sums are in their registers
+                if (t > 0) {   // the first tile finds no sums
+                    asm volatile("s_nop 15");   // the last products' sums are in their registers
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                    for (int i = 0; i < 16; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        scale_sum(o[i], e, keep);
+                        for (int e = 0; e < 16; ++e)
+                            scale_sum(o[i], e, keep);
+                }
             }
         };
         auto maximum = [&]() __attribute__((always_inline)) {
