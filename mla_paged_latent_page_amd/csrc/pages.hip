@@ -188,66 +188,78 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(PageArgs a)
         a.free_count[0] = min(base, a.num_pages);
 }
 
-// Byte offset of position p of request b in a pool, or -1.
-__device__ inline int64_t slot_offset(const PageArgs& a, uint32_t b, uint64_t p, int64_t page_bytes, int64_t token_bytes)
+// The value that lane k holds, in a scalar register.
+__device__ inline uint32_t lane_of(uint32_t v, int k) { return (uint32_t)__builtin_amdgcn_readlane((int)v, k); }
+
+// Page and slot of position p of request b; no page if it has none.  (Always loads: two calls
+// side by side then wait once.)
+__device__ inline void slot_of(const PageArgs& a, uint32_t b, uint64_t p, uint32_t& page, uint32_t& slot)
 {
-    if (p >= (uint64_t)a.max_pages * a.page_size)
-        return -1;
-    const uint32_t lp = (uint32_t)p / a.page_size;
+    const bool there = p < (uint64_t)a.max_pages * a.page_size;
+    const uint32_t q = there ? (uint32_t)p : 0u, lp = q / a.page_size;
     const uint32_t pg = a.page_table[(size_t)b * a.max_pages + lp];
-    if (pg >= a.num_pages)
-        return -1;
-    return (int64_t)pg * page_bytes + (int64_t)((uint32_t)p - lp * a.page_size) * token_bytes;
+    page = there && pg < a.num_pages ? pg : kNoPage;
+    slot = q - lp * a.page_size;
 }
 
-// A thread owns one 16-byte column (or one scale) of one request, layer and kv half and
-// moves it for the accepted rows in ascending order, eight at a time: all eight are read
-// before the first is stored, and a later source a[k] >= k is never an earlier destination
-// i < k, so no thread has to wait for another.  Grid: (columns, layer x kv, request).
-template <typename V>
-__device__ inline void compact_column(const PageArgs& a, char* base, int64_t page_bytes, int64_t token_bytes,
-                                      uint32_t b, uint32_t lo, uint32_t hi)
-{
-    constexpr int U = 8;
-    const uint64_t len = a.cache_len[b];
-    for (uint32_t i0 = lo; i0 < hi; i0 += U) {
-        V v[U];
-        int64_t to[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            to[u] = -1;
-            if (i0 + u < hi) {
-                const uint32_t i = i0 + u - lo, from = a.a[i0 + u];
-                const int64_t src = from == i ? -1 : slot_offset(a, b, len + from, page_bytes, token_bytes);
-                if (src >= 0) {
-                    to[u] = slot_offset(a, b, len + i, page_bytes, token_bytes);
-                    v[u] = *reinterpret_cast<const V*>(base + src);
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (to[u] >= 0)
-                *reinterpret_cast<V*>(base + to[u]) = v[u];
-    }
-}
-
+// A wave owns 64 16-byte columns (or scales) of one request, layer and kv half and moves them
+// for the accepted rows in ascending order, eight rows at a time: all eight are read before the
+// first is stored, and a later source a[k] >= k is never an earlier destination i < k, so no
+// lane has to wait for another.  The pages and slots of 64 rows are looked up at once, one row
+// per lane.  Few rows are bound by the chain of loads (offsets, accepted list, page table, then
+// one round per eight rows): 8 requests, 4 layers 4.0 us, 128 requests, 24 layers of an e4m3 cache
+// 6.6 us; 40 of 60 drafted rows of 64 requests in 24 bf16 layers move at 5.2 TB/s (27 us).
+// Grid: (columns, layer x kv, request).
 constexpr int COMPACT_THREADS = 64;
+template <bool SCALES>
 __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(PageArgs a)
 {
-    const int col = blockIdx.x * COMPACT_THREADS + threadIdx.x;
-    if (col >= a.granules + a.nblk)
-        return;
+    constexpr int U = 8;
+    const int lane = threadIdx.x;
+    const int col = blockIdx.x * COMPACT_THREADS + lane;
+    const bool in_row = col < a.granules, in_scales = SCALES && !in_row && col < a.granules + a.nblk;
+    const int row_col = min(col, a.granules - 1), scale_col = max(min(col - a.granules, a.nblk - 1), 0);
     for (uint32_t b = blockIdx.z; b < a.batch; b += gridDim.z) {
         const uint32_t total = (uint32_t)a.count;
         const uint32_t lo = min(a.b[b], total), hi = min(a.b[b + 1], total);
-        for (uint32_t z = blockIdx.y; z < a.layers * a.kvs; z += gridDim.y) {
-            const int64_t layer = z / a.kvs, kv = z % a.kvs;
-            if (col < a.granules)
-                compact_column<u32x4>(a, a.pool + layer * a.sl + kv * a.sk + (int64_t)col * 16, a.sp, a.st, b, lo, hi);
-            else
-                compact_column<uint32_t>(a, reinterpret_cast<char*>(a.scales + layer * a.ssl + kv * a.ssk + (col - a.granules)),
-                                         a.ssp * 4, a.sst * 4, b, lo, hi);
+        const uint64_t len = a.cache_len[b];
+        for (uint32_t i0 = lo; i0 < hi; i0 += 64) {
+            const int n = (int)min(hi - i0, 64u);
+            const uint32_t i = i0 - lo + lane, from = a.a[i0 + min(lane, n - 1)];
+            uint32_t from_page, from_slot, to_page, to_slot;
+            slot_of(a, b, len + from, from_page, from_slot);
+            slot_of(a, b, len + i, to_page, to_slot);
+            const uint64_t moves = __ballot(lane < n && from != i && from_page != kNoPage && to_page != kNoPage);
+            for (uint32_t z = blockIdx.y; z < a.layers * a.kvs; z += gridDim.y) {
+                const int64_t layer = z / a.kvs, kv = z % a.kvs;
+                char* rows = a.pool + layer * a.sl + kv * a.sk + (int64_t)row_col * 16;
+                float* scales = a.scales + layer * a.ssl + kv * a.ssk + scale_col;
+                for (int k0 = 0; k0 < n; k0 += U) {
+                    // Every lane loads in every round (a branch would wait for the loads before
+                    // it); rows without a move read the pool's first one.
+                    u32x4 v[U];
+                    float s[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool move = moves >> (k0 + u) & 1;
+                        const int64_t page = move ? lane_of(from_page, k0 + u) : 0u;
+                        const int64_t slot = move ? lane_of(from_slot, k0 + u) : 0u;
+                        v[u] = ld16(rows + page * a.sp + slot * a.st);
+                        if constexpr (SCALES)
+                            s[u] = scales[page * a.ssp + slot * a.sst];
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (!(moves >> (k0 + u) & 1))
+                            continue;
+                        const int64_t page = lane_of(to_page, k0 + u), slot = lane_of(to_slot, k0 + u);
+                        if (in_row)
+                            st16(rows + page * a.sp + slot * a.st, v[u]);
+                        if (in_scales)
+                            scales[page * a.ssp + slot * a.sst] = s[u];
+                    }
+                }
+            }
         }
     }
 }
@@ -312,7 +324,8 @@ hipError_t launch_compact(const PageArgs& a, hipStream_t s)
     const unsigned cols = (a.granules + a.nblk + COMPACT_THREADS - 1) / COMPACT_THREADS;
     const dim3 grid(cols, std::min((unsigned)(a.layers * a.kvs), kMaxGridYZ), std::min(a.batch, kMaxGridYZ));
     log_launch("compact_kernel", grid.x * grid.y * grid.z, COMPACT_THREADS, "accepted=%d batch=%u", a.count, a.batch);
-    hipLaunchKernelGGL(compact_kernel, grid, dim3(COMPACT_THREADS), 0, s, a);
+    auto* kernel = a.scales ? compact_kernel<true> : compact_kernel<false>;
+    hipLaunchKernelGGL(kernel, grid, dim3(COMPACT_THREADS), 0, s, a);
     return hipGetLastError();
 }
 

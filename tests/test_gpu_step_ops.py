@@ -483,6 +483,26 @@ def test_compact(dtype, page_size, num_kv):
     assert sc is None or same(cache.scales, sc)
 
 
+@pytest.mark.parametrize("dtype, layers", [("bf16", 2), ("e4m3", 5)])
+def test_compact_long_drafts(dtype, layers):
+    # more accepted rows than a wave has lanes, in one request between two others
+    lens, rng = [3, 77, 40], np.random.default_rng(5)
+    cache, table, _, _ = pages_case(5, lens, 16, dtype, layers=layers, extra=300)
+    picks = [[7], sorted(rng.choice(300, 171, replace=False).tolist()), list(range(64)) + [65, 200]]
+    pool, sc = raw_of(cache.pool).clone(), None if cache.scales is None else cache.scales.clone()
+    for b, p in enumerate(picks):
+        for i, a in enumerate(p):
+            s, d = lens[b] + a, lens[b] + i
+            sp, dp = int(table[b, s // 16]), int(table[b, d // 16])
+            pool[dp, :, :, d % 16] = pool[sp, :, :, s % 16].clone()
+            if sc is not None:
+                sc[dp, :, :, d % 16] = sc[sp, :, :, s % 16].clone()
+    acc = i32(sum(picks, []), "cuda")
+    mp.mla_compact_paged(acc, i32([0, 1, 172, 238], "cuda"), cache)
+    assert same(raw_of(cache.pool), pool)
+    assert sc is None or same(cache.scales, sc)
+
+
 def test_compact_positions_without_a_slot_are_skipped():
     cache, table, _, _ = pages_case(4, [10, 10], 16, "bf16", extra=20)
     before = raw_of(cache.pool).clone()
