@@ -361,7 +361,7 @@ __device__ inline bf16x8 bf16_of_codes(u32x2 v)
     return as_bf16x8(u32x4{two(v[0], lo), two(v[0], hi), two(v[1], lo), two(v[1], hi)});
 }
 
-__device__ inline bf16x8 bf16_of_codes(bf16x8 v) { return v; }
+__device__ inline bf16x8 bf16_of_codes(bf16x8 v) { return v; }   // (no codes)
 
 __device__ inline bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
@@ -457,12 +457,14 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         return FP8 ? (x >> 1 & 1) << 2 | (x >> 3 & 1) << 1 | (x >> 2 & 1) : (x >> 1 & 1) << 2 | (x >> 2 & 1) << 1 | (x >> 3 & 1);
     };
     const uint32_t fk = f(col);
-    // Score operands: bf16: granules 2 s + half of a block, s = 0 .. 3; e4m3: bytes 8 half of
-    // granule 0 (others by exclusive or).
+    // Score operands: granules 2 s + half of a block; bf16: s = 0 .. 3, e4m3: 0 (others by
+    // exclusive or), of a whole block and of the last half one.
     uint32_t k_off[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-        k_off[s] = FP8 ? (s == 0 ? col * 128 + fk * 16 : col * 64 + (col >> 2 & 3) * 16) + half * 8 : col * 128 + (((2 * s + half) ^ fk) * 16);
+        k_off[s] = !FP8    ? col * 128 + (((2 * s + half) ^ fk) * 16)
+                   : s == 0 ? col * 128 + ((half ^ fk) * 16)
+                            : col * 64 + ((half ^ (col >> 2 & 3)) * 16);
     // Transposing reads.  bf16: lane c of a 16-lane group addresses row c / 4 and 8 bytes of its
     // columns; e4m3: row c / 2 of the eight (rows 0 .. 3 and 8 .. 11, + 4 half) and 8 codes.
     [[maybe_unused]] uint32_t v_off[2][2];   // bf16: [feature block parity][rows vrow or vrow + 8]
@@ -514,15 +516,17 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         // SPLIT 2: the join of the item before is done with LDS, the queries' part included.
         if (SPLIT == 2)
             lds_barrier();
-        // Query fragments: lane holds features 16 s + 8 half .. + 7 of its row.
+        // Query fragments: lane holds features 16 s + 8 half .. + 7 of its row; e4m3: 8 (s % 2) .. + 7
+        // of granule s / 2 * 2 + half, as one 16-byte read of codes serves two products.
         constexpr int KEPT = FP8 ? QUERY_KEPT : D / 16;
         bf16x8 q[KEPT];
         char* my_q = FP8 ? smem + QUERY_AT + wave * QUERY_WAVE + lane * 16 : nullptr;
         {
-            const char* src = static_cast<const char*>(a.q) + (int64_t)qrow * (D * 2) + half * 16;
+            const char* src = static_cast<const char*>(a.q) + (int64_t)qrow * (D * 2) + half * (FP8 ? 32 : 16);
+            auto at = [](int s) { return FP8 ? (s >> 1) * 64 + (s & 1) * 16 : s * 32; };
 #pragma unroll
             for (int s = 0; s < KEPT; ++s)
-                q[s] = as_bf16x8(ld16(src + s * 32));
+                q[s] = as_bf16x8(ld16(src + at(s)));
             if (flip)
 #pragma unroll
                 for (int s = 0; s < KEPT; ++s)
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     u32x4 v[7];
 #pragma unroll
                     for (int s = 0; s < 7; ++s)
-                        v[s] = ld16(src + (s0 + s) * 32);
+                        v[s] = ld16(src + at(s0 + s));
 #pragma unroll
                     for (int s = 0; s < 7; ++s)
                         lds_st16(my_q + (s0 + s - KEPT) * 1024, v[s] ^ flip);
@@ -790,23 +794,23 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         // Fragments are read KD products ahead; `between(k)` is other work during product k.
         // e4m3: codes become bf16 on the way to the matrix cores; each block
         // of 128 columns has sums of its own, times the block's scale of each row.
-        constexpr int KN = D / 16, KD = FP8 ? 5 : 6, VN = 2 * (K / 32), VD = 4;
+        constexpr int KN = D / 16, KD = FP8 ? 3 : 6, VN = 2 * (K / 32), VD = 4;   // e4m3: KD reads, two products each
         using Frag = std::conditional_t<FP8, u32x2, bf16x8>;
+        using KFrag = std::conditional_t<FP8, u32x4, bf16x8>;
         auto scores = [&](uint32_t t, auto between) __attribute__((always_inline)) {
             const char* st = smem + stage_of(t);
             // Exclusive or of the granule after the sum with the stage: it is not worth keeping.
             [[maybe_unused]] const uint32_t at8[2] = {stage_of(t) + k_off[0], stage_of(t) + k_off[1]};
-            auto frag = [&](int k) __attribute__((always_inline)) -> Frag {
+            auto frag = [&](int k) __attribute__((always_inline)) -> KFrag {
                 if constexpr (FP8)
-                    return *reinterpret_cast<const u32x2*>(
-                        smem + (at8[k >> 5] ^ ((k < 32 ? k & 7 : k & 3) * 16)) + (k >> 3) * BLOCK_BYTES);
+                    return lds_ld16(smem + (at8[k >> 4] ^ ((k < 16 ? k & 3 : k & 1) * 32)) + (k >> 2) * BLOCK_BYTES);
                 else
                     return as_bf16x8(lds_ld16(st + k_off[k & 3] + (k >> 2) * BLOCK_BYTES));
             };
             auto query = [&](int k) __attribute__((always_inline)) { return as_bf16x8(lds_ld16(my_q + (k - KEPT) * 1024)); };
             const uint32_t scale_row = FP8 ? scales_at(t) : 0;
             f32x16 acc, part;
-            Frag kf[KD];
+            KFrag kf[KD];
             bf16x8 qx[2];
             f32x4 bs[4];
 #pragma unroll
@@ -820,7 +824,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 constexpr bool end = k == KN - 1 || (FP8 && at == 7);
                 f32x16& sum = blk == 0 ? acc : part;
                 // (the conversion runs in the shadow of the product before)
-                const bf16x8 x = bf16_of_codes(kf[k % KD]);
+                bf16x8 x;
+                if constexpr (FP8) {
+                    const u32x4 two = kf[(k >> 1) % KD];
+                    x = bf16_of_codes(k & 1 ? u32x2{two[2], two[3]} : u32x2{two[0], two[1]});
+                } else {
+                    x = kf[k % KD];
+                }
                 bf16x8 y;
                 if constexpr (k < KEPT)
                     y = q[k];
@@ -832,7 +842,9 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     sum = mfma_last<FP8>(sum, x, y);
                 else
                     mfma_next<FP8>(sum, x, y);
-                if constexpr (k + KD < KN)
+                if constexpr (FP8 && (k & 1) && (k >> 1) + KD < KN / 2)
+                    kf[(k >> 1) % KD] = frag((k >> 1) + KD);
+                if constexpr (!FP8 && k + KD < KN)
                     kf[k % KD] = frag(k + KD);
                 if constexpr (FP8 && k + 2 >= KEPT && k + 2 < KN)
                     qx[k % 2] = query(k + 2);
