@@ -23,9 +23,10 @@ constexpr int SCALES_WAVE = 256;             // 5 blocks x 8 rows, floats
 constexpr int SCALES = WAVES * SCALES_WAVE;
 constexpr int SCALES_AT = STAGES * STAGE8;
 constexpr int QUERY_AT = SCALES_AT + STAGES * SCALES;
-constexpr int QUERY_KEPT = 15;               // fragments in registers; the others are in LDS
+constexpr int QUERY_KEPT = 28;               // fragments in registers; the others are in LDS
 constexpr int QUERY_WAVE = (D / 16 - QUERY_KEPT) * 1024;
-constexpr int SMEM8 = QUERY_AT + WAVES * QUERY_WAVE;
+constexpr int JOIN_WAVE = 8 * 16 * 256 + 256; // a wave's half of the output sums, maxima and sums (SPLIT 2)
+constexpr int SMEM8 = std::max(QUERY_AT + WAVES * QUERY_WAVE, WAVES * JOIN_WAVE);
 static_assert(SMEM8 <= 163840 && STAGES * STAGE <= 163840, "LDS");
 constexpr int PIECE_WAVE = 32 * (K + 2);     // floats of one wave's partial result: 32 rows, maximum, sum
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -305,32 +306,23 @@ __device__ inline void wait_loads()
 
 // One product with its sums in ordinary registers: the output sums take all 256 accumulation
 // registers, and the compiler would put these there too.  It does not see that this is a matrix
-// instruction, so each one waits two states for operands just written by vector instructions,
-// and the last one of a chain for its result before anything can read it (12 wait states after
-// 8 passes; back-to-back products into the same registers need none).  Nor must it move the
-// sums inside a chain: tests/test_matrix_waits.py reads the generated code for that.
-template <bool FRESH>   // operands just written by vector instructions
+// instruction, so the last one of a chain waits for its result before anything can read it (12
+// wait states after 8 passes; back-to-back products into the same registers need none), and no
+// operand may come from a vector instruction in the two states before.  Nor must it move the
+// sums inside a chain: tests/test_matrix_waits.py reads the generated code for both.
 __device__ inline void mfma_first(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    if constexpr (FRESH)
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
-    else
-        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
+    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(acc) : "v"(x), "v"(y));
 }
-template <bool FRESH>
 __device__ inline void mfma_next(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    if constexpr (FRESH)
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
-    else
-        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
+    asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(acc) : "v"(x), "v"(y));
 }
-// FRESH: into the same registers; else into others, where the result stays.
-template <bool FRESH>
+template <bool IN_PLACE>   // else into other registers, where the result stays
 __device__ inline f32x16 mfma_last(f32x16& acc, bf16x8 x, bf16x8 y)
 {
-    if constexpr (FRESH) {
-        asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
+    if constexpr (IN_PLACE) {
+        asm("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\ts_nop 13" : "+v"(acc) : "v"(x), "v"(y));
         return acc;
     } else {
         f32x16 out;
@@ -360,8 +352,6 @@ __device__ inline bf16x8 bf16_of_codes(u32x2 v)
     const std::true_type hi;
     return as_bf16x8(u32x4{two(v[0], lo), two(v[0], hi), two(v[1], lo), two(v[1], hi)});
 }
-
-__device__ inline bf16x8 bf16_of_codes(bf16x8 v) { return v; }   // (no codes)
 
 __device__ inline bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
@@ -533,15 +523,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     q[s] = as_bf16x8(__builtin_bit_cast(u32x4, q[s]) ^ flip);
             if constexpr (FP8) {
 #pragma unroll
-                for (int s0 = KEPT; s0 < D / 16; s0 += 7) {
-                    u32x4 v[7];
-#pragma unroll
-                    for (int s = 0; s < 7; ++s)
-                        v[s] = ld16(src + at(s0 + s));
-#pragma unroll
-                    for (int s = 0; s < 7; ++s)
-                        lds_st16(my_q + (s0 + s - KEPT) * 1024, v[s] ^ flip);
-                }
+                for (int s = KEPT; s < D / 16; ++s)
+                    lds_st16(my_q + (s - KEPT) * 1024, ld16(src + at(s)) ^ flip);
             }
         }
         // The stages of the item before are no longer read (and no load into them is in flight:
@@ -816,6 +799,15 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 #pragma unroll
             for (int k = 0; k < KD; ++k)
                 kf[k] = frag(k);
+            [[maybe_unused]] auto converted = [&](int k) __attribute__((always_inline)) {
+                if constexpr (FP8) {
+                    const u32x4 two = kf[(k >> 1) % KD];
+                    return bf16_of_codes(k & 1 ? u32x2{two[2], two[3]} : u32x2{two[0], two[1]});
+                } else {
+                    return bf16x8{};
+                }
+            };
+            [[maybe_unused]] bf16x8 xn = converted(0);
             between(std::integral_constant<int, -1>{});
             __builtin_amdgcn_sched_barrier(0);
             each<KN>([&](auto index) __attribute__((always_inline)) {
@@ -823,11 +815,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 constexpr int blk = FP8 ? k >> 3 : 0, at = FP8 ? k & 7 : k;
                 constexpr bool end = k == KN - 1 || (FP8 && at == 7);
                 f32x16& sum = blk == 0 ? acc : part;
-                // (the conversion runs in the shadow of the product before)
+                // (the next product's codes are converted first: its operands are never just written)
                 bf16x8 x;
                 if constexpr (FP8) {
-                    const u32x4 two = kf[(k >> 1) % KD];
-                    x = bf16_of_codes(k & 1 ? u32x2{two[2], two[3]} : u32x2{two[0], two[1]});
+                    x = xn;
+                    if constexpr (k + 1 < KN)
+                        xn = converted(k + 1);
+                    __builtin_amdgcn_sched_barrier(0);
                 } else {
                     x = kf[k % KD];
                 }
@@ -837,12 +831,12 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 else
                     y = qx[k % 2];
                 if (at == 0)
-                    mfma_first<FP8>(sum, x, y);
+                    mfma_first(sum, x, y);
                 else if (end)
                     sum = mfma_last<FP8>(sum, x, y);
                 else
-                    mfma_next<FP8>(sum, x, y);
-                if constexpr (FP8 && (k & 1) && (k >> 1) + KD < KN / 2)
+                    mfma_next(sum, x, y);
+                if constexpr (FP8 && (k & 1) == 0 && (k >> 1) + KD < KN / 2)
                     kf[(k >> 1) % KD] = frag((k >> 1) + KD);
                 if constexpr (!FP8 && k + KD < KN)
                     kf[k % KD] = frag(k + KD);
@@ -998,15 +992,30 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                     block_weights(i);
                 }
             }
+            [[maybe_unused]] bf16x8 vn;
+            if constexpr (FP8) {
+                vn = bf16_of_codes(vf[0]);
+                vf[0] = vfrag(VD);
+            }
             each<VN>([&](auto index) __attribute__((always_inline)) {
                 constexpr int v = index;
                 if constexpr (v == 0 || (FP8 && (v & 7) == 0)) {
                     pf[0] = as_bf16x8(u32x4{pk[0], pk[1], pk[2], pk[3]});
                     pf[1] = as_bf16x8(u32x4{pk[4], pk[5], pk[6], pk[7]});
                 }
-                o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf16_of_codes(vf[v % VD]), pf[v & 1], o[v >> 1], 0, 0, 0);
-                if constexpr (v + VD < VN)
-                    vf[v % VD] = vfrag(v + VD);
+                if constexpr (FP8) {
+                    const bf16x8 x = vn;
+                    if constexpr (v + 1 < VN)
+                        vn = bf16_of_codes(vf[(v + 1) % VD]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, pf[v & 1], o[v >> 1], 0, 0, 0);
+                    if constexpr (v + 1 + VD < VN)
+                        vf[(v + 1) % VD] = vfrag(v + 1 + VD);
+                } else {
+                    o[v >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[v % VD], pf[v & 1], o[v >> 1], 0, 0, 0);
+                    if constexpr (v + VD < VN)
+                        vf[v % VD] = vfrag(v + VD);
+                }
                 if constexpr (SPLIT == 1) {
                     if constexpr (v % 8 == 3 && v / 8 < GROUPS)
                         load(std::integral_constant<int, v / 8>{}, 0);
@@ -1043,12 +1052,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         } else {
             // The two waves of the same rows join their results: each hands the other half of its
             // sums through LDS, and keeps the half it stores.
-            constexpr int WAVE_BYTES = 8 * 16 * 256 + 256;
-            static_assert(WAVES * WAVE_BYTES <= sizeof(smem), "LDS");
+            static_assert(WAVES * JOIN_WAVE <= sizeof(smem), "LDS");
             auto join = [&](auto first) __attribute__((always_inline)) {
                 constexpr int keep = first, give = 8 - keep;
-                char* mine = smem + wave * WAVE_BYTES;
-                const char* other = smem + (wave ^ 2) * WAVE_BYTES;
+                char* mine = smem + wave * JOIN_WAVE;
+                const char* other = smem + (wave ^ 2) * JOIN_WAVE;
                 lds_barrier();   // the stages are no longer read
                 each<32>([&](auto index) __attribute__((always_inline)) {
                     constexpr int q = index, fb = give + q / 4, i = q % 4;
