@@ -23,7 +23,7 @@ constexpr int SCALES_WAVE = 256;             // 5 blocks x 8 rows, floats
 constexpr int SCALES = WAVES * SCALES_WAVE;
 constexpr int SCALES_AT = STAGES * STAGE8;
 constexpr int QUERY_AT = SCALES_AT + STAGES * SCALES;
-constexpr int QUERY_KEPT = 28;               // fragments in registers; the others are in LDS
+constexpr int QUERY_KEPT = 26;               // fragments in registers; the others are in LDS
 constexpr int QUERY_WAVE = (D / 16 - QUERY_KEPT) * 1024;
 constexpr int JOIN_WAVE = 8 * 16 * 256 + 256; // a wave's half of the output sums, maxima and sums (SPLIT 2)
 constexpr int SMEM8 = std::max(QUERY_AT + WAVES * QUERY_WAVE, WAVES * JOIN_WAVE);
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         // Fragments are read KD products ahead; `between(k)` is other work during product k.
         // e4m3: codes become bf16 on the way to the matrix cores; each block
         // of 128 columns has sums of its own, times the block's scale of each row.
-        constexpr int KN = D / 16, KD = FP8 ? 3 : 6, VN = 2 * (K / 32), VD = 4;   // e4m3: KD reads, two products each
+        constexpr int KN = D / 16, KD = FP8 ? 4 : 8, VN = 2 * (K / 32), VD = 8;   // e4m3: KD reads, two products each
         using Frag = std::conditional_t<FP8, u32x2, bf16x8>;
         using KFrag = std::conditional_t<FP8, u32x4, bf16x8>;
         auto scores = [&](uint32_t t, auto between) __attribute__((always_inline)) {
