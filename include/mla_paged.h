@@ -701,7 +701,7 @@ mla_status_t mla_write_latent_paged_fp8_at(const void* kv_input, const uint32_t*
  *                 share.  Nothing in it has to start at zero.  Calls that may overlap (other
  *                 streams, captured graphs replayed side by side) need workspaces of their own.
  * Rows of 576 columns with K = 512 on BF16 or e4m3 caches run on the matrix cores; other
- * shapes and F32 run one wave per token and head.
+ * shapes and F32 run 4 or 16 waves per token and head, which read each row for it alone.
  */
 size_t mla_tree_attention_workspace_size(int32_t total_tokens, int32_t num_heads, int32_t K);
 mla_status_t mla_tree_attention_paged(const void* q_latent, const uint32_t* input_row_offsets,
