@@ -1,7 +1,10 @@
 // Page upkeep of a paged cache: copies of pages, forks of requests, compaction of
 // accepted rows, and the return of pages without references.  Bit copies of 16-byte
 // pieces over all layers and kv halves; every kernel is bound by memory or, for a few
-// rows, by its chain of index loads.
+// rows, by its chain of index loads.  Forking 16 parents to 112 children in 16 layers:
+// 30 us for 278 MB (children of one parent read its page from the caches); a few beams: 3.5 us.
+// Freeing: 5 to 11 us for the references, one compare-and-swap per page, and 3 to 4 us
+// for the walk over all counts, which keeps the list in order.
 #include <algorithm>
 
 #include "step.hpp"
