@@ -21,8 +21,8 @@
 //   12 requests of 17-33 tokens x 128 heads, 1300-6000 rows, bf16: 250-285 + 26 us, 860 TFLOP/s.
 //     Bound by the matrix cores (52 % busy) and by what a single wave per SIMD can issue between
 //     their instructions, at the clock the power limit leaves.
-//   64 requests of one token x 128 heads, 256-4096 rows, bf16: 52 + 17 us.  Bound by memory: 129
-//     MB read and 91 MB written (84 MB of it partial results), then 72 MB read by the join.
+//   64 requests of one token x 128 heads, 256-4096 rows, bf16: 50 + 12 us.  Bound by memory and its
+//     latency: the rows, the queries of every share, and the partial results, written and read.
 //   5 requests of 5-8 tokens x 16 heads, 78-94 thousand rows, e4m3: 150-170 + 14 us.  Bound by
 //     instruction issue: each wave converts every tile's codes to bf16 (272 conversions next to
 //     68 products); 80-96 of an item's 128 rows hold queries.
@@ -91,6 +91,7 @@ struct MfmaParams {
     uint32_t ps_magic, ps_shift;             // p / page_size = mulhi(p, magic) >> shift for p < 2^31
     uint32_t piece;                          // floats of a partial result slot
     Cut* cuts;                               // [kAttnGroups]
+    uint32_t twins;                          // SPLIT 2: workgroups that share an item's rows
     uint32_t groups;                         // of 32 rows in an item: 4, or 2
     int min_tiles;                           // least steps of a workgroup's share
 };
@@ -104,12 +105,13 @@ __device__ inline uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdg
 
 // How a workgroup's four waves share an item.  SPLIT 1: 128 query rows, 32 per wave, every wave
 // reads all tiles.  SPLIT 2: 64 query rows, two pairs of waves; a step takes two tiles, one per
-// pair, and the pairs' results are joined at the end.  An item counts as COST units before its
+// pair, and the pairs' results are joined at the end; with twins, an item has 128 rows and two
+// workgroups of one XCD take 64 each, at the same time from the same cache rows.  An item counts as COST units before its
 // steps' one each: fetching its queries, filling the ring and writing its results takes about as
 // long as that many steps.
 template <int SPLIT>
 struct Shape {
-    static constexpr uint32_t ROWS = kAttnRows / SPLIT;   // query rows of an item
+    static constexpr uint32_t ROWS = kAttnRows / SPLIT;   // query rows of a workgroup
     static constexpr uint32_t STEP = TILE * SPLIT;        // cache rows of a step
     static constexpr uint32_t COST = 8;
 };
@@ -121,7 +123,7 @@ struct Request {
 };
 
 template <int SPLIT>
-__device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
+__device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t twins, uint32_t b)
 {
     Request r{};
     const uint32_t end = min(a.iro[a.L.batch], (uint32_t)a.T);
@@ -131,7 +133,8 @@ __device__ inline Request request_at(const TreeAttentionArgs& a, uint32_t b)
     r.n = t1 > r.t0 ? t1 - r.t0 : 0;
     r.cached = min(a.cache_len[b], a.capacity);
     r.len = min(r.cached + r.n, a.capacity);
-    r.nm = (r.n * (uint32_t)a.H + Shape<SPLIT>::ROWS - 1) / Shape<SPLIT>::ROWS;   // n * H below 2^31 / D
+    const uint32_t rows = Shape<SPLIT>::ROWS * twins;
+    r.nm = (r.n * (uint32_t)a.H + rows - 1) / rows;   // n * H below 2^31 / D
     r.nu = (r.len + Shape<SPLIT>::STEP - 1) / Shape<SPLIT>::STEP + Shape<SPLIT>::COST;
     return r;
 }
@@ -164,6 +167,7 @@ template <int SPLIT>
 struct Schedule {
     static constexpr uint32_t COST = Shape<SPLIT>::COST;
     const TreeAttentionArgs& a;
+    uint32_t twins;
     int lane;
     uint32_t total, groups, share, rest, snap;
     uint32_t first;                          // first request in the lanes
@@ -177,12 +181,12 @@ struct Schedule {
         before = tiles_before;
         mine = Request{};
         if (b0 + lane < a.L.batch)
-            mine = request_at<SPLIT>(a, b0 + lane);
+            mine = request_at<SPLIT>(a, twins, b0 + lane);
         scan = wave_inclusive(mine.nm * mine.nu);
     }
     __device__ uint32_t loaded() const { return (uint32_t)__builtin_amdgcn_readlane((int)scan, 63); }
 
-    __device__ Schedule(const TreeAttentionArgs& args, int l, uint32_t min_tiles) : a(args), lane(l)
+    __device__ Schedule(const MfmaParams& P, int l) : a(P.a), twins(SPLIT == 1 ? 1 : P.twins), lane(l)
     {
         load(0, 0);
         total = loaded();
@@ -192,8 +196,8 @@ struct Schedule {
         }
         if (a.L.batch > 64)
             load(0, 0);
-        const uint32_t want = (total + min_tiles - 1) / min_tiles;
-        groups = want < 1 ? 1u : want > kAttnGroups ? (uint32_t)kAttnGroups : want;
+        const uint32_t want = (total + P.min_tiles - 1) / P.min_tiles, most = kAttnGroups / twins;
+        groups = want < 1 ? 1u : want > most ? most : want;
         share = groups == kAttnGroups ? total / kAttnGroups : total / groups;
         rest = total - share * groups;
         snap = share / 32;
@@ -442,12 +446,13 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
     // The wave's 32 query rows, and its tile of each step.
     const uint32_t qwave = SPLIT == 1 ? wave : wave & 1, pair = SPLIT == 1 ? 0 : wave >> 1;
 
-    Schedule<SPLIT> sched(a, lane, P.min_tiles);
+    Schedule<SPLIT> sched(P, lane);
+    const uint32_t twins = sched.twins, twin = twins == 1 ? 0 : blockIdx.x >> 3 & 1;
     // Neighbouring shares go to one XCD (block i runs on XCD i % 8): items of one request
     // then read the same rows through one L2.
-    const uint32_t per = (sched.groups + 7) / 8;
-    const uint32_t w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    const bool idle = (blockIdx.x >> 3) >= per || w >= sched.groups || sched.total == 0;
+    const uint32_t per = (sched.groups + 7) / 8, at = twins == 1 ? blockIdx.x >> 3 : blockIdx.x >> 4;
+    const uint32_t w = (blockIdx.x & 7) * per + at;
+    const bool idle = at >= per || w >= sched.groups || sched.total == 0;
     Request r{};
     uint32_t stop = sched.total, u = 0;
     Cut rec{};
@@ -460,11 +465,11 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
             if (u != lo)   // (an end of an item may be a cut, within `snap` of it)
                 rec = Cut{w, sched.first_cut_past(lo + COST + sched.snap),
                           sched.first_cut_past(lo + r.nu - sched.snap - 1) - 1,
-                          r.t0 * (uint32_t)a.H + m * ROWS, r.n * (uint32_t)a.H - m * ROWS, {}};
+                          r.t0 * (uint32_t)a.H + m * ROWS * twins, r.n * (uint32_t)a.H - m * ROWS * twins, {}};
         }
     }
-    if (threadIdx.x == 0)
-        P.cuts[blockIdx.x] = rec;
+    if (threadIdx.x == 0 && twin == 0)
+        P.cuts[at * 8 + (blockIdx.x & 7)] = rec;
     if (idle)
         return;
 
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
     while (u < stop) {
         while (u >= r.base + r.nm * r.nu) {
             const uint32_t next = r.base + r.nm * r.nu;
-            r = request_at<SPLIT>(a, r.b + 1);
+            r = request_at<SPLIT>(a, twins, r.b + 1);
             r.base = next;
             r = uniform(r);
         }
@@ -528,8 +533,10 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         const uint32_t table_row = r.b * a.L.max_pages;   // checked on the host: below 2^32
 
         const uint32_t rows = r.n * (uint32_t)a.H;                 // below 2^31 / D
-        const uint32_t row = m * ROWS + qwave * 32 + col;
-        const bool live = uniform(m * ROWS + qwave * 32) < rows;
+        const uint32_t block0 = (m * twins + twin) * ROWS, row = block0 + qwave * 32 + col;
+        if (SPLIT == 2 && block0 >= rows)
+            continue;   // no rows for this twin
+        const bool live = uniform(block0 + qwave * 32) < rows;
         const bool valid = row < rows;
         const uint32_t qrow = r.t0 * (uint32_t)a.H + min(row, rows - 1);
         const uint32_t tok = min(row, rows - 1) / (uint32_t)a.H;   // token of the request
@@ -1077,7 +1084,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 
         l += swap32(l);
         const bool whole = tile0 == 0 && tile1 + COST == r.nu;
-        float* piece = a.ws + (size_t)(2 * w + (tile0 == 0 ? 1 : 0)) * P.piece + (size_t)qwave * PIECE_WAVE;
+        float* piece = a.ws + (size_t)(2 * w + (tile0 == 0 ? 1 : 0)) * P.piece +
+                       (size_t)(SPLIT == 1 ? qwave : twin * 2 + qwave) * PIECE_WAVE;
         if constexpr (SPLIT == 1) {
             store_result<0, 16>(a, o, mref, l, qrow, valid, whole, piece, lane);
         } else {
@@ -1321,14 +1329,20 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind,
         P.ps_magic = (uint32_t)(((uint64_t(1) << (31 + sh)) + ps - 1) / ps);
         P.ps_shift = sh - 1;
     }
-    // Two pairs of waves where an average request fills no more than half of a wide item.  Wide /
-    // two pairs, us: 16 requests x 16 heads x 3-4 tokens, 20-40 thousand rows: e4m3 190 / 133, bf16
-    // 148 / 146; 64 x 16 heads, 256-4096 rows: e4m3 67 / 50, bf16 53 / 43.  Above, they are slower:
-    // 16 x 16 heads x 5-6 tokens: e4m3 194 / 211, bf16 162 / 206 (each item reads all of its rows);
-    // 64 x 128 heads, bf16: 70 / 75.
-    const bool split = (int64_t)a.T * a.H <= (int64_t)Shape<2>::ROWS * a.L.batch;
-    P.groups = split ? 2 : 4;
-    const int64_t waves = (std::min<int64_t>((int64_t)a.T * a.H, (int64_t)P.groups * 32) + 31) / 32;
+    // Two pairs of waves where an average request fills no more than half of a wide item, and two
+    // such workgroups side by side where it fills no more than one: they leave partial results of
+    // half as many shares.  Wide / two pairs, us: 16 requests x 16 heads x 3-4 tokens, 20-40 thousand
+    // rows: e4m3 187 / 136, bf16 151 / 147; 64 x 16 heads, 256-4096 rows: e4m3 64 / 50, bf16 54 / 43.
+    // Wide / two workgroups: 64 x 128 heads, 256-4096 rows: e4m3 80 / 75, bf16 70 / 62; 2 x 128 heads,
+    // 60-120 thousand rows: e4m3 101 / 89, bf16 90 / 75; 16 x 16 heads x 8 tokens, 20-40 thousand rows:
+    // e4m3 235 / 235, bf16 188 / 193, and x 5-6 tokens, bf16 165 / 181 (their loads run
+    // only one step ahead).
+    const int64_t query_rows = (int64_t)a.T * a.H;
+    const bool split = query_rows <= (int64_t)kAttnRows * a.L.batch;
+    const bool twins = split && query_rows > (int64_t)Shape<2>::ROWS * a.L.batch;
+    P.twins = twins ? 2 : 1;
+    P.groups = split && !twins ? 2 : 4;
+    const int64_t waves = (std::min<int64_t>(query_rows, (int64_t)P.groups * 32) + 31) / 32;
     P.piece = (uint32_t)(waves * PIECE_WAVE);
     P.min_tiles = split ? 2 : 4;   // steps: 4 tiles either way
     P.cuts = reinterpret_cast<Cut*>(a.ws + (size_t)2 * kAttnGroups * P.piece);
@@ -1346,7 +1360,7 @@ hipError_t launch_tree_attention_mfma(const TreeAttentionArgs& a, AttnKind kind,
     if (hipError_t e = hipGetLastError())
         return e;
     // One block per cut and 32 rows of an item.
-    const unsigned join_blocks = kAttnGroups * P.groups;
+    const unsigned join_blocks = kAttnGroups / P.twins * P.groups;
     log_launch("tree_attention_join", join_blocks, 256, "T=%d H=%d", a.T, a.H);
     hipLaunchKernelGGL(tree_attention_join, dim3(join_blocks), dim3(256), 0, s, P);
     return hipGetLastError();

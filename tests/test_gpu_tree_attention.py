@@ -23,25 +23,32 @@ NARROW = [
     ([1000, 20, 20, 20], [12, 1, 1, 1], 16, 16, "chain"),   # three items of one request
     ([2049, 4095], [1, 2], 33, 8, "tree"),
 ]
-WIDE = [
-    ([9000, 3], [8, 20], 16, 100, "tree"),
+# At most 128: two workgroups side by side.
+TWINS = [
     ([30000], [1], 128, 16, "chain"),
     ([0, 0], [2, 1], 64, 5, "chain"),
     ([300], [5], 13, 64, "tree"),                   # 65 rows
+    ([2000, 10, 700], [12, 1, 5], 16, 16, "tree"),  # 192, 16 and 80 rows
+    ([5000, 0, 63], [8, 0, 8], 16, 100, "holes"),
+    ([12345, 1], [3, 1], 64, 128, "tree"),
+]
+WIDE = [
+    ([9000, 3], [8, 20], 16, 100, "tree"),
     ([64, 64], [10, 9], 16, 40, "holes"),
     ([500], [600], 16, 128, "chain"),
+    ([20000, 7], [9, 1], 64, 16, "tree"),
 ]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-@pytest.mark.parametrize("lens, new, heads, page_size, mask", NARROW + WIDE)
+@pytest.mark.parametrize("lens, new, heads, page_size, mask", NARROW + TWINS + WIDE)
 def test_shares(lens, new, heads, page_size, mask, dtype):
     case = AttentionCase(heads + lens[0], lens, new, heads, page_size=page_size, mask=mask, dtype=dtype)
     check_attention(case, *attend(case))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
-@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("heads", [16, 100, 220])
 def test_more_requests_than_lanes(heads, dtype):
     rng = np.random.default_rng(heads)
     lens, new = rng.integers(0, 300, 150), rng.choice([0, 1, 1, 2], 150)
