@@ -152,9 +152,9 @@ def test_two_graphs_at_once():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             run()
-        runs.append((graph, torch.cuda.Stream(), out, z, ref))
+        runs.append((graph, torch.cuda.Stream(), out, z, ref, run))   # (run holds the graph's workspace)
     for _ in range(5):
-        for graph, stream, out, z, _ in runs:
+        for graph, stream, out, *_ in runs:
             out.zero_()
             stream.wait_stream(torch.cuda.current_stream())
         for graph, stream, *_ in runs:
@@ -162,5 +162,5 @@ def test_two_graphs_at_once():
                 graph.replay()
                 graph.replay()
         torch.cuda.synchronize()
-        for graph, stream, out, z, ref in runs:
+        for graph, stream, out, z, ref, _ in runs:
             assert same(out, ref[0]) and same(z, ref[1])
