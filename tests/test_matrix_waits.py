@@ -100,7 +100,7 @@ def violations(stream):
     return bad, seen
 
 
-def test_the_checker_sees_mistakes():
+def test_the_rules_see_mistakes():
     head = "_Z1tree_attention_mfma1:\n"
     chain = " v_mfma_f32_32x32x16_bf16 v[0:15], v[16:19], v[20:23], 0\n" \
             " v_mfma_f32_32x32x16_bf16 v[0:15], v[24:27], v[20:23], v[0:15]\n"
