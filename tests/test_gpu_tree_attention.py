@@ -164,3 +164,51 @@ def test_two_graphs_at_once():
         torch.cuda.synchronize()
         for graph, stream, out, z, ref, _ in runs:
             assert same(out, ref[0]) and same(z, ref[1])
+
+
+@pytest.mark.parametrize("heads, page_size", [(16, 64), (128, 64), (128, 60)])
+def test_far_pages_of_an_e4m3_cache(heads, page_size):
+    # page offsets past 2^32 bytes, and past 2^27 floats in the scales
+    pages = 130000
+    case = AttentionCase(30, [150], [2], heads, page_size=page_size, dtype="e4m3")
+    out, z = attend(case)
+    pool = torch.zeros((pages, 1, 1, page_size, 1, 576), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((pages, 1, 1, page_size, 5), device="cuda")
+    far = [pages - 1, 3, pages - 4000]
+    for i, f in enumerate(far):
+        page = int(case.host.page_table[0, i])
+        pool[f, 0] = case.dev.pool[page, 1]
+        scales[f, 0] = case.dev.scales[page, 1]
+    table = torch.tensor([far], dtype=torch.int32, device="cuda")
+    got, gz = torch.empty_like(out), torch.empty_like(z)
+    ws = torch.empty(mp.mla_tree_attention_workspace_size(2, heads, 512), dtype=torch.uint8, device="cuda")
+    mp.mla_tree_attention_paged_fp8_cache(case.q, case.iro, None, case.scale, 512,
+                                          mp.PagedKVCache(pool, table, case.dev.cache_lengths, scales=scales), 0, got,
+                                          ws, lse=gz)
+    assert same(out, got) and same(z, gz)
+
+
+def test_far_pages_of_the_page_calls():
+    # 8 GiB of pages: copies, forks and compaction across offsets past 2^32 bytes
+    ps, pages, layers = 64, 29200, 4
+    pool = torch.zeros((pages, layers, 1, ps, 1, 576), dtype=torch.bfloat16, device="cuda")
+    far = pages - 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pool[far] = torch.randn((layers, 1, ps, 1, 576), generator=g, device="cuda").to(torch.bfloat16)
+    want = pool[far].clone()
+    table = torch.tensor([[far], [-1]], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([40, 0], dtype=torch.int32, device="cuda")
+    cache = mp.PagedKVCache(pool, table, lengths)
+
+    def ids(*a):
+        return torch.tensor(a, dtype=torch.int32, device="cuda")
+    mp.mla_copy_pages(ids(far), ids(0), cache)
+    assert same(pool[0], want)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[far] = 1
+    mp.mla_fork_paged(ids(0), ids(1), ids(far - 1), refs, cache)
+    assert same(pool[far - 1][:, :, :40], want[:, :, :40]) and bool((pool[far - 1][:, :, 40:] == 0).all())
+    mp.mla_compact_paged(ids(3, 9), ids(0, 2, 2), cache)
+    want[:, :, 40], want[:, :, 41] = want[:, :, 43].clone(), want[:, :, 49].clone()
+    assert same(pool[far], want)
+    assert not bool(pool[1:far - 1].view(torch.int16).any())
