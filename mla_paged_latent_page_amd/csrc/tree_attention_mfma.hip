@@ -15,7 +15,8 @@
 //
 // Work: every workgroup takes an equal share of all tiles of all requests (one workgroup per
 // CU); shares that end inside an item leave their sums, maximum and sum in the workspace in
-// binary32, and tree_attention_join adds them up in a fixed order.
+// binary32, and tree_attention_join adds them up in a fixed order.  Requests with few query rows
+// take narrower items, whose cache rows two pairs of waves share (Shape).
 //
 // Measured (MI355X, main kernel + join):
 //   12 requests of 17-33 tokens x 128 heads, 1300-6000 rows, bf16: 250-285 + 26 us, 860 TFLOP/s.
@@ -23,9 +24,9 @@
 //     their instructions, at the clock the power limit leaves.
 //   64 requests of one token x 128 heads, 256-4096 rows, bf16: 50 + 12 us.  Bound by memory and its
 //     latency: the rows, the queries of every share, and the partial results, written and read.
-//   5 requests of 5-8 tokens x 16 heads, 78-94 thousand rows, e4m3: 150-170 + 14 us.  Bound by
+//   5 requests of 5-8 tokens x 16 heads, 78-94 thousand rows, e4m3: 150-185 + 11 us.  Bound by
 //     instruction issue: each wave converts every tile's codes to bf16 (272 conversions next to
-//     68 products); 80-96 of an item's 128 rows hold queries.
+//     68 products); 80-128 of an item's 128 rows hold queries.
 //   4 requests of one token x 16 heads, 100-600 rows, bf16: 15 + 6 us, a chain of loads
 //     (offsets, page ids, rows) and two launches.
 // An e4m3 product with the queries split into two e4m3 parts would need no conversion, but the
