@@ -679,6 +679,9 @@ mla_status_t mla_write_latent_paged_fp8_at(const void* kv_input, const uint32_t*
  *
  * What a row that a token does not see holds (NaN and infinities included) does not change
  * that token's output; neither does anything behind a request's last drafted row.
+ * Of the rows it does see, a score of NaN or +infinity makes the token's whole output and
+ * lse NaN; a score of -infinity is a weight of 0, which makes NaN of the output columns in
+ * which that row is not finite, and of no other.
  *
  * q_latent        [device] [total_tokens][num_heads][D_c], D_c the cache's row width; bf16
  *                 with a BF16 cache, float with an F32 cache
@@ -713,7 +716,8 @@ mla_status_t mla_tree_attention_paged(const void* q_latent, const uint32_t* inpu
 /*
  * mla_tree_attention_paged on an e4m3 cache: row_p[c] = code * scale of its block of 128
  * columns.  The codes go into the products as they are (bf16 holds every e4m3 value); the
- * scales multiply the scores' block sums and the weights, in binary32.
+ * scales multiply the scores' block sums and the weights, in binary32 (an infinite scale
+ * thus makes a block's sum infinite, and its 128 columns NaN for the tokens that see the row).
  *
  * q_latent, out_latent  bf16
  * cache           dtype F8E4M3FN, D_c % 16 == 0

@@ -59,7 +59,8 @@ constexpr int QUERY_KEPT = 26;               // fragments in registers; the othe
 constexpr int QUERY_WAVE = (D / 16 - QUERY_KEPT) * 1024;
 constexpr int JOIN_WAVE = 8 * 16 * 256 + 256; // a wave's half of the output sums, maxima and sums (SPLIT 2)
 constexpr int SMEM8 = std::max(QUERY_AT + WAVES * QUERY_WAVE, WAVES * JOIN_WAVE);
-static_assert(SMEM8 <= 163840 && STAGES * STAGE <= 163840, "LDS");
+constexpr int FLAG_BYTES = 16;               // behind all of it: whether clear_nonfinite found something
+static_assert(SMEM8 + FLAG_BYTES <= 163840 && STAGES * STAGE + FLAG_BYTES <= 163840, "LDS");
 constexpr int PIECE_WAVE = 32 * (K + 2);     // floats of one wave's partial result: 32 rows, maximum, sum
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -437,7 +438,9 @@ __device__ __attribute__((always_inline)) inline void store_result(const TreeAtt
 template <bool PAGE8, bool FP8, int SPLIT>
 __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams P)
 {
-    __shared__ __attribute__((aligned(1024))) char smem[FP8 ? SMEM8 : STAGES * STAGE];
+    constexpr int FLAG_AT = FP8 ? SMEM8 : STAGES * STAGE;
+    __shared__ __attribute__((aligned(1024))) char smem[FLAG_AT + FLAG_BYTES];
+    uint32_t* const cleared = reinterpret_cast<uint32_t*>(smem + FLAG_AT);
     constexpr int LOADS = FP8 ? 6 : BLOCKS;   // LDS loads of 8 rows
     constexpr uint32_t ROWS = Shape<SPLIT>::ROWS, STEP = Shape<SPLIT>::STEP, COST = Shape<SPLIT>::COST;
     const TreeAttentionArgs& a = P.a;
@@ -570,6 +573,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
         // the last step waited for all of them, and those behind the last tile are switched off).
         if (SPLIT == 1)
             lds_barrier();
+        if (threadIdx.x == 0)
+            *cleared = 0;   // (every wave has read the last item's; there is a barrier before it is set)
 
         // Loads of one tile: this wave fetches rows 8 i .. 8 i + 7 for its one or two bands i,
         // lane l granule l % 8 of every block of row l / 8.  Rows past the end repeat the last one.
@@ -705,7 +710,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
 
         // Drafted rows may be hidden from some tokens and hold anything: a weight of 0 would turn
         // their infinities and NaN into NaN, so those become 0 here, between the scores and the
-        // weighted sums of step t (a token that sees such a row has a NaN weight for it already).
+        // weighted sums of step t, and `cleared` is set.  (A token that sees such a row has a NaN
+        // weight for it, but one of 0 where its score is -infinity: restored at the end.)
         auto clear_nonfinite = [&](uint32_t t) __attribute__((always_inline)) {
             if ((tile0 + t + 1) * STEP <= cached || !(r.n > 1 || a.mask))
                 return;
@@ -716,7 +722,8 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 char* mine = smem + stage_of(t) + band(i) * 1024 + lane * 16;
                 if (p0 + band(i) * 8 + (lane >> 3) >= cached)
                     for (int j = 0; j < K / (FP8 ? 128 : 64); ++j) {
-                        u32x4 v = lds_ld16(mine + j * BLOCK_BYTES);
+                        const u32x4 was = lds_ld16(mine + j * BLOCK_BYTES);
+                        u32x4 v = was;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if constexpr (FP8) {   // bytes of 0x7F or 0xFF
@@ -727,11 +734,17 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                                 v[e] = nonfinite16(v[e] >> 16) ? v[e] & 0xFFFFu : v[e];
                             }
                         }
-                        lds_st16(mine + j * BLOCK_BYTES, v);
+                        if (((was[0] ^ v[0]) | (was[1] ^ v[1]) | (was[2] ^ v[2]) | (was[3] ^ v[3])) != 0) {
+                            lds_st16(mine + j * BLOCK_BYTES, v);
+                            *cleared = 1;
+                        }
                     }
                 if (FP8 && lane < 40 && p0 + band(i) * 8 + (lane & 7) >= cached) {
                     float* sc = reinterpret_cast<float*>(smem + SCALES_AT + stage_no(t) * SCALES + band(i) * SCALES_WAVE) + lane;
-                    *sc = fabsf(*sc) < INFINITY ? *sc : 0.0f;
+                    if (!(fabsf(*sc) < INFINITY)) {
+                        *sc = 0.0f;
+                        *cleared = 1;
+                    }
                 }
             }
             lds_barrier();
@@ -1128,6 +1141,49 @@ __global__ void __launch_bounds__(64 * WAVES, 1) tree_attention_mfma(MfmaParams 
                 join(std::integral_constant<int, 0>{});
             else
                 join(std::integral_constant<int, 8>{});
+        }
+        // What clear_nonfinite took from the tokens that see it: 0 times infinity (or NaN) is NaN in
+        // the columns where a row they see is not finite.  Written over the features that the wave
+        // stored: only a broken row comes here, and the wave has no registers to spare before.
+        if (tile1 * STEP > cached && (r.n > 1 || a.mask) && uniform(*cleared)) {
+            wait_loads<0>();   // (stores too: other lanes stored some of these values)
+            const uint32_t ln = lane_again();
+            const uint32_t mine = block0 + qwave * 32 + (ln & 31), there = min(mine, rows - 1);
+            const uint32_t token = there / (uint32_t)a.H, column = 4 * (ln >> 5);
+            uint16_t* out = static_cast<uint16_t*>(a.out) + ((int64_t)r.t0 * a.H + there) * K + column;
+#pragma unroll 1
+            for (uint32_t p = max(tile0 * STEP, cached); p < min(tile1 * STEP, len); ++p) {
+                const uint32_t j = p - cached;
+                const bool sees = a.mask ? j < 64u * (uint32_t)a.words &&
+                                               (a.mask[(int64_t)(r.t0 + token) * a.words + (j >> 6)] >> (j & 63)) & 1
+                                         : j <= token;
+                if (!sees || mine >= rows)
+                    continue;
+                const char* row_p = a.L.base + token_offset(a.L, r.b, p) + column * (FP8 ? 1 : 2);
+#pragma unroll 1
+                for (uint32_t q = pair * 32; q < pair * 32 + 64 / SPLIT; ++q) {   // features 8 q + column .. + 3
+                    uint32_t broken;   // a bit for each
+                    if constexpr (FP8) {
+                        const uint32_t x = *reinterpret_cast<const uint32_t*>(row_p + q * 8);
+                        const float* scale = reinterpret_cast<const float*>(a.Ls.base + token_offset(a.Ls, r.b, p)) + (q >> 4);
+                        broken = 0;
+                        for (int e = 0; e < 4; ++e)
+                            broken |= (uint32_t)((x >> (8 * e) & 0x7F) == 0x7F) << e;
+                        broken = fabsf(*scale) < INFINITY ? broken : 15;
+                    } else {
+                        const u32x2 x = *reinterpret_cast<const u32x2*>(row_p + q * 16);
+                        broken = nonfinite16(x[0]) | nonfinite16(x[0] >> 16) << 1 | nonfinite16(x[1]) << 2 |
+                                 nonfinite16(x[1] >> 16) << 3;
+                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (broken >> e & 1) {
+                            if (whole)
+                                out[q * 8 + e] = 0x7FC0;
+                            else
+                                piece[(q * 64 + ln) * 4 + e] = NAN;
+                        }
+                }
+            }
         }
     }
 }

@@ -1,0 +1,118 @@
+"""The drafted step's calls at the ends of their documented ranges."""
+import math
+
+import pytest
+import torch
+
+from plain_step import HALF_BF16, U32, AttentionCase
+from test_gpu_step_ops import attend
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite in a row that is seen
+# ---------------------------------------------------------------------------
+def row_at(case, b, p):
+    """Cache row at position p of request b, and its scales."""
+    ps = case.host.page_size
+    page, slot = int(case.host.page_table[b, p // ps]), p % ps
+    return case.dev.pool[page, case.layer, 0, slot, 0], (case.dev.scales[page, case.layer, 0, slot]
+                                                         if case.host.dtype == "e4m3" else None)
+
+
+def without(case, drop):
+    """float64 outputs, log-sum-exps and their bounds (those of AttentionCase.reference) where no
+    token sees position drop[b] of request b; and which tokens saw it."""
+    out = torch.zeros((case.T, case.H, case.K), dtype=torch.float64, device="cuda")
+    lse, tol, ltol = torch.zeros_like(out[..., 0]), torch.zeros_like(out), torch.zeros_like(out[..., 0])
+    saw, at = torch.zeros(case.T, dtype=torch.bool, device="cuda"), 0
+    for b, n in enumerate(case.new.tolist()):
+        rows, cached = case.rows64(b), int(case.lens[b])
+        for i in range(n):
+            p = list(range(cached)) + [cached + j for j in range(n) if (case.seen[b][i] >> j) & 1]
+            saw[at + i] = drop[b] in p
+            r = rows[[x for x in p if x != drop[b]]]
+            q = case.q[at + i].double()
+            s = (q @ r.t().contiguous()) * case.scale
+            ds = ((q.abs() @ r.abs().t().contiguous()) * case.scale).amax(dim=1) * (case.D + 8) * U32
+            z = torch.logsumexp(s, dim=1)
+            w = torch.exp(s - z[:, None])
+            o, mag = w @ r[:, :case.K], w @ r[:, :case.K].abs()
+            rel = 2 * ds + 2.0 ** -20 + 3 * r.shape[0] * U32 + (0.0 if case.host.dtype == "f32" else HALF_BF16)
+            out[at + i], lse[at + i] = o, z
+            tol[at + i] = mag * rel[:, None] + o.abs() * (2 * U32 if case.host.dtype == "f32" else HALF_BF16) * 1.02 + 1e-30
+            ltol[at + i] = ds + 2.0 ** -20 + 3 * r.shape[0] * U32 + z.abs() * 2 * U32
+        at += n
+    return out, lse, tol, ltol, saw
+
+
+INFINITE = [
+    # lens, new, heads, page_size, mask
+    ([70, 33], [3, 4], 16, 16, "chain"),       # narrow items
+    ([70, 33], [3, 4], 16, 5, "tree"),
+    ([150, 40], [2, 1], 100, 16, "tree"),      # two workgroups side by side
+    ([70, 9], [9, 40], 16, 16, "tree"),        # wide
+    ([33, 300], [20, 5], 64, 12, "chain"),
+    ([9000, 5000], [2, 3], 16, 64, "tree"),    # split items
+    ([4000, 64], [9, 40], 16, 128, "tree"),
+]
+
+
+@pytest.mark.parametrize("where", ["drafted", "cached"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("lens, new, heads, page_size, mask", INFINITE)
+def test_an_infinity_in_a_row_that_is_seen(lens, new, heads, page_size, mask, dtype, where):
+    """Score + infinity or NaN: the output is NaN.  Score - infinity: the weight is 0, and 0 times
+    infinity is NaN in the columns the infinity is in (e4m3: those of the block whose scale it is)
+    and there alone.  Other tokens do not notice."""
+    case = AttentionCase(sum(lens) + heads, lens, new, heads, page_size=page_size, mask=mask, dtype=dtype)
+    # the row of the first drafted token (seen by it and its descendants), or of a cached one
+    drop = [l if where == "drafted" else l // 2 for l in lens]
+    out, lse, tol, ltol, saw = without(case, drop)
+    bad = torch.zeros(case.K, dtype=torch.bool, device="cuda")
+    if dtype == "e4m3":
+        # All products of block 2 have one sign: positive codes there, and queries of one sign per head.
+        block = slice(256, 384)
+        sign = torch.where(torch.arange(heads, device="cuda") % 2 == 0, 1.0, -1.0).to(case.q.dtype)
+        case.q[:, :, block] = (case.q[:, :, block].abs() + 0.01) * sign[:, None]
+        out, lse, tol, ltol, saw = without(case, drop)
+        bad[block] = True
+        up = (sign > 0).expand(case.T, heads)
+        for b in range(2):
+            row, sc = row_at(case, b, drop[b])
+            row[block] = 0x38          # 1.0
+            sc[2] = math.inf
+    else:
+        column = 77
+        bad[column] = True
+        up = case.q[:, :, column] > 0
+        assert bool((case.q[:, :, column] != 0).all())
+        for b in range(2):
+            row_at(case, b, drop[b])[0][column] = math.inf
+    got, z = attend(case)
+    live = int(case.new.sum())
+    got, z, up = got[:live].double(), z[:live].double(), up[:live]
+    finite = ~(saw[:, None] & up)
+    assert bool((saw[:, None] & up).any()) and bool((saw[:, None] & ~up).any())
+    assert bool(torch.isnan(got[~finite]).all()) and bool(torch.isnan(z[~finite]).all())
+    nan = (saw[:, None] & ~up)[:, :, None] & bad
+    assert bool(torch.isnan(got[nan]).all()), "a weight of 0 times infinity is NaN"
+    ok = finite[:, :, None] & ~nan
+    assert bool(((got - out).abs()[ok] <= tol[ok]).all())
+    assert bool(((z - lse).abs()[finite] <= ltol[finite]).all())
+
+
+@pytest.mark.parametrize("heads, new", [(16, [2, 3]), (128, [1, 2]), (16, [9, 20])])
+def test_an_infinity_in_rope_columns_has_no_column_of_the_output(heads, new):
+    case = AttentionCase(heads, [100, 31], new, heads, mask="chain")
+    case.seen = [[(1 << (i + 1)) - 1 for i in range(n)] for n in new]
+    drop = [100, 31]
+    out, lse, tol, ltol, saw = without(case, drop)
+    for b in range(2):
+        row_at(case, b, drop[b])[0][520] = math.inf
+    got, z = attend(case)
+    finite = case.q[:, :, 520] < 0
+    assert bool(saw.all()) and bool(torch.isnan(got[~finite]).all())
+    assert bool(((got.double() - out).abs()[finite] <= tol[finite]).all())
+    assert bool(((z.double() - lse).abs()[finite] <= ltol[finite]).all())
