@@ -686,7 +686,8 @@ mla_status_t mla_write_latent_paged_fp8_at(const void* kv_input, const uint32_t*
  * q_latent        [device] [total_tokens][num_heads][D_c], D_c the cache's row width; bf16
  *                 with a BF16 cache, float with an F32 cache
  * input_row_offsets [device] uint32 [batch_size+1], [0] = 0, nondecreasing; rows of q_latent
- *                 at or past input_row_offsets[batch_size] are neither read nor written to
+ *                 at or past input_row_offsets[batch_size] are neither read nor written to.
+ *                 Where they do decrease the outputs are unspecified.
  * total_tokens    [host] T >= input_row_offsets[batch_size]
  * num_heads       query heads, >= 1; T * num_heads * D_c < 2^31
  * tree_mask       [device] uint64 [total_tokens][mask_words], 8-byte aligned, or NULL.

@@ -164,7 +164,8 @@ __device__ inline uint32_t wave_inclusive(uint32_t v)
 // The schedule: all units (of all items of all requests, in that order) in equal shares.  A
 // cut that falls within `snap` tiles of an item's first or last one is moved there: the item
 // is then not split for so little.  Every wave works it out for itself; the requests of the last 64
-// looked at stay in its lanes.  The host has checked that the units number below 2^31.
+// looked at stay in its lanes.  The host has checked that the units of ascending offsets number
+// below 2^31; offsets that decrease can name a token in many requests, so nothing is done for them.
 template <int SPLIT>
 struct Schedule {
     static constexpr uint32_t COST = Shape<SPLIT>::COST;
@@ -186,16 +187,25 @@ struct Schedule {
             mine = request_at<SPLIT>(a, twins, b0 + lane);
         scan = wave_inclusive(mine.nm * mine.nu);
     }
+    // Some offset among those of the 64 requests from b0 on is above the next one.
+    __device__ bool decreasing(uint32_t b0) const
+    {
+        return __ballot(b0 + lane < a.L.batch && a.iro[b0 + lane] > a.iro[b0 + lane + 1]) != 0;
+    }
     __device__ uint32_t loaded() const { return (uint32_t)__builtin_amdgcn_readlane((int)scan, 63); }
 
     __device__ Schedule(const MfmaParams& P, int l) : a(P.a), twins(SPLIT == 1 ? 1 : P.twins), lane(l)
     {
         load(0, 0);
         total = loaded();
+        bool bad = decreasing(0);
         for (uint32_t b0 = 64; b0 < a.L.batch; b0 += 64) {
             load(b0, total);
             total += loaded();
+            bad |= decreasing(b0);
         }
+        if (bad)
+            total = 0;
         if (a.L.batch > 64)
             load(0, 0);
         const uint32_t want = (total + P.min_tiles - 1) / P.min_tiles, most = kAttnGroups / twins;

@@ -4,7 +4,9 @@ import math
 import pytest
 import torch
 
-from plain_step import HALF_BF16, U32, AttentionCase
+import mla_paged_latent_page_amd as mp
+from gpu_util import check_guards, guarded_empty
+from plain_step import HALF_BF16, U32, AttentionCase, check_attention, i32
 from test_gpu_step_ops import attend
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +118,34 @@ def test_an_infinity_in_rope_columns_has_no_column_of_the_output(heads, new):
     assert bool(saw.all()) and bool(torch.isnan(got[~finite]).all())
     assert bool(((got.double() - out).abs()[finite] <= tol[finite]).all())
     assert bool(((z.double() - lse).abs()[finite] <= ltol[finite]).all())
+
+
+# ---------------------------------------------------------------------------
+# offsets out of order
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_offsets_that_decrease_stay_inside_the_outputs(heads, dtype):
+    case = AttentionCase(heads, [70, 33, 5, 90], [3, 4, 1, 2], heads, mask="tree", dtype=dtype)
+    good = case.iro
+    for offsets in ([0, 7, 3, 8, 10], [4, 0, 10, 2, 9], [0, 10, 0, 10, 10], [0, 0xFFFFFFFF, 1, 2, 3], [9, 8, 7, 6, 5]):
+        case.iro = i32(offsets, "cuda")
+        attend(case)           # (the guards beside outputs and workspace)
+    case.iro = good
+    check_attention(case, *attend(case))
+
+
+def test_offsets_that_name_every_token_in_every_second_request():
+    # as many units of work as pass 2^32 when each request is believed
+    T, heads, requests, ps = 2000, 128, 2000, 128
+    case = AttentionCase(1, [1], [1], heads, page_size=ps)
+    q = torch.zeros((T, heads, 576), dtype=torch.bfloat16, device="cuda")
+    out = guarded_empty((T, heads, 512), torch.bfloat16)
+    lse = guarded_empty((T, heads), torch.float32)
+    ws = guarded_empty((mp.mla_tree_attention_workspace_size(T, heads, 512),), torch.uint8)
+    table = torch.zeros((requests, 1024), dtype=torch.int32, device="cuda")
+    lengths = torch.full((requests,), 1024 * ps - 5, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, T] * (requests // 2) + [T], dtype=torch.int32, device="cuda")
+    mp.mla_tree_attention_paged(q, offsets, None, 0.1, 512, mp.PagedKVCache(case.dev.pool, table, lengths), 1, out, ws,
+                                lse=lse)
+    check_guards("tree attention")
