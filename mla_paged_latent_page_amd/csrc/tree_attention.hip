@@ -9,6 +9,7 @@
 // each score is a wave sum, with the running maximum and sum of the softmax in binary32, and
 // the waves' results are joined in LDS.  Bound by its arithmetic: each row is read for one
 // head at a time.
+#include <algorithm>
 #include <type_traits>
 
 #include "step.hpp"
@@ -69,14 +70,15 @@ __device__ inline void load8(const char* row, int col, float scale, float (&x)[8
 }
 
 template <AttnKind KIND, int SPLIT>
-__global__ void __launch_bounds__(64 * SPLIT) tree_attention_general(TreeAttentionArgs a)
+__global__ void __launch_bounds__(64 * SPLIT) tree_attention_general(TreeAttentionArgs a, uint32_t first_pair)
 {
     constexpr bool F32 = KIND == ATTN_F32;
     constexpr AttnKind QKIND = F32 ? ATTN_F32 : ATTN_BF16;
     constexpr int EB = F32 ? 4 : 2;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const uint32_t pair = first_pair + blockIdx.x;   // below 2^31 / D
+    const int t = pair / (uint32_t)a.H, h = pair % (uint32_t)a.H;
     const uint32_t end = min(a.iro[a.L.batch], (uint32_t)a.T);
     if ((uint32_t)t >= end)
         return;
@@ -212,8 +214,7 @@ hipError_t launch_tree_attention(const TreeAttentionArgs& a, AttnKind kind, hipS
     // 429 / 442, 2048 pairs 754 / 748, 8192 pairs over 1024 rows 1351 / 1202.
     const int64_t pairs = (int64_t)a.T * a.H;
     const bool many = pairs <= 1024;
-    const unsigned blocks = (unsigned)pairs, threads = many ? 1024 : 256;   // below 2^31 / D blocks
-    log_launch("tree_attention_general", blocks, threads, "T=%d H=%d K=%d D=%d kind=%d", a.T, a.H, a.K, a.D, (int)kind);
+    const unsigned threads = many ? 1024 : 256;
     auto pick = [&](auto k) {
         constexpr AttnKind kd = decltype(k)::value;
         return many ? tree_attention_general<kd, 16> : tree_attention_general<kd, 4>;
@@ -221,8 +222,16 @@ hipError_t launch_tree_attention(const TreeAttentionArgs& a, AttnKind kind, hipS
     auto* kernel = kind == ATTN_F32    ? pick(std::integral_constant<AttnKind, ATTN_F32>{})
                    : kind == ATTN_BF16 ? pick(std::integral_constant<AttnKind, ATTN_BF16>{})
                                        : pick(std::integral_constant<AttnKind, ATTN_E4M3>{});
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), 0, s, a);
-    return hipGetLastError();
+    // A launch holds less than 2^32 threads in a dimension, and drops those past them without an error.
+    constexpr int64_t kMostBlocks = int64_t(1) << 23;
+    for (int64_t first = 0; first < pairs; first += kMostBlocks) {
+        const unsigned blocks = (unsigned)std::min(pairs - first, kMostBlocks);
+        log_launch("tree_attention_general", blocks, threads, "T=%d H=%d K=%d D=%d kind=%d", a.T, a.H, a.K, a.D, (int)kind);
+        hipLaunchKernelGGL(kernel, dim3(blocks), dim3(threads), 0, s, a, (uint32_t)first);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace mla

@@ -149,3 +149,44 @@ def test_offsets_that_name_every_token_in_every_second_request():
     mp.mla_tree_attention_paged(q, offsets, None, 0.1, 512, mp.PagedKVCache(case.dev.pool, table, lengths), 1, out, ws,
                                 lse=lse)
     check_guards("tree attention")
+
+
+# ---------------------------------------------------------------------------
+# more work-items than one launch holds (2^32 in a dimension)
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype, T, H", [("bf16", (1 << 20) + 3, 16), ("bf16", 3, (1 << 24) // 3 + 9), ("e4m3", 1 << 22, 5)])
+def test_attention_of_more_than_2_24_pairs(dtype, T, H):
+    # rows of 16 columns; the table holds one page of 8 positions
+    D, K, ps = 16, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((T, H, D), generator=g, device="cuda").to(torch.bfloat16)
+    if dtype == "e4m3":
+        pool = torch.randn((2, 1, 1, ps, 1, D), generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+        scales = torch.rand((2, 1, 1, ps, 1), generator=g, device="cuda") + 0.5
+        rows = pool[1, 0, 0, :, 0].view(torch.float8_e4m3fn).float() * scales[1, 0, 0]
+    else:
+        pool, scales = torch.randn((2, 1, 1, ps, 1, D), generator=g, device="cuda").to(torch.bfloat16), None
+        rows = pool[1, 0, 0, :, 0].float()
+    cache = mp.PagedKVCache(pool, i32([[1]], "cuda"), i32([6], "cuda"), scales=scales)
+    out = torch.full((T, H, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    ws = torch.empty(mp.mla_tree_attention_workspace_size(T, H, K), dtype=torch.uint8, device="cuda")
+    call = mp.mla_tree_attention_paged if scales is None else mp.mla_tree_attention_paged_fp8_cache
+    call(q, i32([0, T], "cuda"), None, 0.25, K, cache, 0, out, ws, lse=lse)
+    pick = torch.unique(torch.cat([torch.randint(0, T * H, (4000,), generator=g, device="cuda"),
+                                   torch.arange(T * H - 500, T * H, device="cuda"), torch.arange(500, device="cuda"),
+                                   torch.arange((1 << 23) - 50, (1 << 23) + 50, device="cuda"),
+                                   torch.arange((1 << 24) - 50, (1 << 24) + 50, device="cuda")]))
+    pick = pick[pick < T * H]
+    x = q.view(-1, D)[pick].double()
+    r = rows.double()
+    s = x @ r.t().contiguous() * 0.25
+    last = 6 + (pick // H).clamp(max=1)             # the newest position that the token sees
+    s = torch.where(torch.arange(ps, device="cuda")[None] <= last[:, None], s, -math.inf)
+    ref = torch.softmax(s, 1) @ r[:, :K]
+    mag = torch.softmax(s, 1) @ r[:, :K].abs()
+    ds = ((x.abs() @ r.abs().t().contiguous()) * 0.25).amax(1) * (D + 8) * U32
+    tol = mag * (2 * ds + 2.0 ** -20 + 3 * ps * U32)[:, None] + ref.abs() * HALF_BF16 * 1.02 + 1e-30
+    assert bool(((out.view(-1, K)[pick].double() - ref).abs() <= tol).all())
+    z = torch.logsumexp(s, 1)
+    assert bool(((lse.view(-1)[pick].double() - z).abs() <= ds + 2.0 ** -20 + 3 * ps * U32 + z.abs() * 2 * U32).all())
