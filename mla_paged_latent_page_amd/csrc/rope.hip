@@ -194,12 +194,26 @@ hipError_t launch_rope_freqs(const RopeFreqsArgs& a, hipStream_t s)
 
 hipError_t launch_rope_q(const RopeQArgs& a, bool f32, bool half, hipStream_t s)
 {
-    const dim3 grid(a.T, (a.H + HEADS_PER_BLOCK - 1) / HEADS_PER_BLOCK);
-    log_launch("rope_q_kernel", grid.x * grid.y, 256, "T=%d H=%d R=%d f32=%d half=%d", a.T, a.H, a.R, f32, half);
+    // A launch holds less than 2^32 threads in a dimension, and drops those past them without an error;
+    // 65,535 blocks is the portable limit of the second one.
+    constexpr int kMostTokens = 1 << 23, kMostHeads = 65535 * HEADS_PER_BLOCK;
     auto* kernel = f32 ? (half ? rope_q_kernel<true, true> : rope_q_kernel<true, false>)
                        : (half ? rope_q_kernel<false, true> : rope_q_kernel<false, false>);
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    for (int64_t t0 = 0; t0 < a.T; t0 += kMostTokens)
+        for (int64_t h0 = 0; h0 < a.H; h0 += kMostHeads) {
+            RopeQArgs c = a;
+            c.T = (int)std::min<int64_t>(a.T - t0, kMostTokens);
+            c.H = (int)std::min<int64_t>(a.H - h0, kMostHeads);
+            c.q += t0 * a.q_st + h0 * a.q_sh;
+            c.out += t0 * a.o_st + h0 * a.o_sh;
+            c.pos += t0;
+            const dim3 grid(c.T, (c.H + HEADS_PER_BLOCK - 1) / HEADS_PER_BLOCK);
+            log_launch("rope_q_kernel", grid.x * grid.y, 256, "T=%d H=%d R=%d f32=%d half=%d", c.T, c.H, c.R, f32, half);
+            hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c);
+            if (hipError_t e = hipGetLastError())
+                return e;
+        }
+    return hipSuccess;
 }
 
 }  // namespace mla

@@ -5,9 +5,10 @@ import pytest
 import torch
 
 import mla_paged_latent_page_amd as mp
+import workloads as W
 from gpu_util import check_guards, guarded_empty
 from plain_step import HALF_BF16, U32, AttentionCase, check_attention, i32
-from test_gpu_step_ops import attend
+from test_gpu_step_ops import attend, same
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +191,26 @@ def test_attention_of_more_than_2_24_pairs(dtype, T, H):
     assert bool(((out.view(-1, K)[pick].double() - ref).abs() <= tol).all())
     z = torch.logsumexp(s, 1)
     assert bool(((lse.view(-1)[pick].double() - z).abs() <= ds + 2.0 ** -20 + 3 * ps * U32 + z.abs() * 2 * U32).all())
+
+
+@pytest.mark.parametrize("T, H, half", [((1 << 24) + 5, 1, False), (1, (1 << 22) + 70, True), (2, (1 << 22) + 70, False)])
+def test_rope_q_of_more_than_one_grid(T, H, half):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    R = 16
+    q = torch.randn((T, H, 8 + R), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.from_numpy(W.rope_table(500, R)).cuda()
+    pos = torch.randint(0, 500, (T,), generator=g, device="cuda").to(torch.int32)
+    out = torch.full_like(q, 7.0)
+    mp.mla_rope_q(q, pos, table, out, d_nope=8, layout="half" if half else "interleaved")
+    assert same(out[..., :8], q[..., :8])
+    for lo in range(0, T * H, 1 << 22):
+        x = q.view(-1, 8 + R)[lo:lo + (1 << 22), 8:].double()
+        tab = table.double()[pos[torch.arange(lo, lo + x.shape[0], device="cuda") // H].long()]
+        c, s = tab[:, 0::2], tab[:, 1::2]
+        x0, x1 = x.chunk(2, 1) if half else (x[:, 0::2], x[:, 1::2])
+        y0, y1 = x0 * c - x1 * s, x0 * s + x1 * c
+        m0, m1 = (x0 * c).abs() + (x1 * s).abs(), (x0 * s).abs() + (x1 * c).abs()
+        y = out.view(-1, 8 + R)[lo:lo + (1 << 22), 8:].double()
+        g0, g1 = y.chunk(2, 1) if half else (y[:, 0::2], y[:, 1::2])
+        for got, ref, mag in ((g0, y0, m0), (g1, y1, m1)):
+            assert bool(((got - ref).abs() <= mag * 2 * U32 + ref.abs() * HALF_BF16 * 1.01).all())
