@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(NT, 1) kv_matmul_ring(KvRingParams P)
             int64_t off = -1;
             if (t < a.T) {
                 const uint32_t b = find_request(a.iro, a.L.batch, (uint32_t)t);
-                const uint32_t p = a.cache_len[b] + ((uint32_t)t - a.iro[b]);
-                off = store_offset(a.L, b, p);
+                const uint32_t first = a.cache_len[b], p = first + ((uint32_t)t - a.iro[b]);
+                off = p < first ? -1 : store_offset(a.L, b, p);   // (no position past 2^32)
             }
             rowoff[r] = off;
         }

@@ -141,12 +141,13 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(typename
     for (int k = 0; k < TW; ++k) {
         const uint32_t t = (uint32_t)min(t0 + k, a.T - 1);
         const uint32_t b = cnt[k] == 0 ? 0u : min(cnt[k], a.L.batch) - 1;
-        const uint32_t p = a.cache_len[b] + (t - a.iro[b]);
+        const uint32_t first = a.cache_len[b], p = first + (t - a.iro[b]);
         uint32_t pr = p;
         if constexpr (AT)
             pr = a.pos[t];
         const uint32_t pf = pr < (uint32_t)a.max_seq ? pr : (uint32_t)a.max_seq - 1;   // freqs row, clamped
-        off[k] = store_offset(a.L, b, p);   // -1: no slot for this position, nothing is stored
+        // -1: no slot for this position (or it is past 2^32), nothing is stored
+        off[k] = p < first ? -1 : store_offset(a.L, b, p);
         soff[k] = FP8 ? store_offset(a.Ls, b, p) : 0;
         const float* f = a.freqs + (int64_t)pf * a.R + pair0 * 2;
         fr0[k] = rot ? *reinterpret_cast<const f32x4*>(f) : f32x4{0.f, 0.f, 0.f, 0.f};

@@ -1,6 +1,7 @@
 """The drafted step's calls at the ends of their documented ranges."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -8,7 +9,7 @@ import mla_paged_latent_page_amd as mp
 import workloads as W
 from gpu_util import check_guards, guarded_empty
 from plain_step import HALF_BF16, U32, AttentionCase, check_attention, i32
-from test_gpu_step_ops import attend, same
+from test_gpu_step_ops import attend, cache_of, raw_of, same
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +215,37 @@ def test_rope_q_of_more_than_one_grid(T, H, half):
         g0, g1 = y.chunk(2, 1) if half else (y[:, 0::2], y[:, 1::2])
         for got, ref, mag in ((g0, y0, m0), (g1, y1, m1)):
             assert bool(((got - ref).abs() <= mag * 2 * U32 + ref.abs() * HALF_BF16 * 1.01).all())
+
+
+# ---------------------------------------------------------------------------
+# positions
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_latent_writes_past_position_2_32_store_nothing(dtype, half):
+    case = W.latent_write_case("far", seed=3, seq_lens=[6, 3], start_lengths=[0, 20], page_size=16, K=512, R=64,
+                               dtype=dtype, max_seq_len=100)
+    dc, t = W.device_latent_write(case)
+    dc.cache_lengths.copy_(i32([2 ** 32 - 2, 2 ** 32 - 1], "cuda"))
+    before, scales = raw_of(dc.pool).clone(), None if dc.scales is None else dc.scales.clone()
+    args = (t["gamma"], case.eps, t["freqs"], 512, cache_of(dc), 1)
+    layout = "half" if half else "interleaved"
+    if dtype == "e4m3":
+        mp.mla_write_latent_paged_fp8_at(t["x"], t["input_row_offsets"], i32(np.arange(9), "cuda"), *args, layout=layout)
+        mp.mla_write_latent_paged_fp8(t["x"], t["input_row_offsets"], *args)
+    else:
+        mp.mla_write_latent_paged_at(t["x"], t["input_row_offsets"], i32(np.arange(9), "cuda"), *args, layout=layout)
+        mp.mla_write_latent_paged(t["x"], t["input_row_offsets"], *args)
+    assert same(raw_of(dc.pool), before)
+    assert scales is None or same(dc.scales.view(torch.int32), scales.view(torch.int32))
+
+
+@pytest.mark.parametrize("heads", [1, 2])
+def test_kv_products_past_position_2_32_store_nothing(heads):
+    case = W.kv_matmul_case("far", seed=1, seq_lens=[6, 300], start_lengths=[0, 20], hidden_dim=256, num_kv_heads=heads,
+                            head_dim=128, page_size=16)
+    dc, t = W.device_kv(case)
+    dc.cache_lengths.copy_(i32([2 ** 32 - 2, 2 ** 32 - 299], "cuda"))
+    before = raw_of(dc.pool).clone()
+    mp.kv_matmul_paged(t["hidden"], t["input_row_offsets"], t["weight"], cache_of(dc), case.layer_idx)
+    assert same(raw_of(dc.pool), before)
