@@ -84,12 +84,12 @@ template <>
 struct WriteArgs<true> { using type = LatentWriteAtArgs; };
 
 template <bool FP8, bool AT, bool HALF>
-__global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(typename WriteArgs<AT>::type a)
+__global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(typename WriteArgs<AT>::type a, int first)
 {
     constexpr int TW = TOKENS_PER_WAVE;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t0 = (blockIdx.x * WRITE_WAVES + wave) * TW;
+    const int t0 = first + (blockIdx.x * WRITE_WAVES + wave) * TW;
     if (t0 >= a.T)
         return;
     const bool lat = lane * 8 < a.K;   // K <= 512: at most 64 lanes
@@ -269,10 +269,17 @@ template <bool FP8, bool AT, bool HALF = false>
 static hipError_t launch(const typename WriteArgs<AT>::type& a, const char* name, hipStream_t s)
 {
     constexpr int per_block = WRITE_WAVES * TOKENS_PER_WAVE;
-    const unsigned grid = (a.T + per_block - 1) / per_block;
-    log_launch(name, grid, 64 * WRITE_WAVES, "T=%d K=%d R=%d", a.T, a.K, a.R);
-    hipLaunchKernelGGL((latent_write_kernel<FP8, AT, HALF>), dim3(grid), dim3(64 * WRITE_WAVES), 0, s, a);
-    return hipGetLastError();
+    // A launch holds less than 2^32 threads in a dimension, and drops those past them without an error.
+    constexpr int64_t kMostTokens = int64_t(1) << 26;
+    for (int64_t first = 0; first < a.T; first += kMostTokens) {
+        const int64_t tokens = a.T - first < kMostTokens ? a.T - first : kMostTokens;
+        const unsigned grid = (unsigned)((tokens + per_block - 1) / per_block);
+        log_launch(name, grid, 64 * WRITE_WAVES, "T=%d K=%d R=%d", a.T, a.K, a.R);
+        hipLaunchKernelGGL((latent_write_kernel<FP8, AT, HALF>), dim3(grid), dim3(64 * WRITE_WAVES), 0, s, a, (int)first);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_latent_write(const LatentWriteArgs& a, hipStream_t s)

@@ -249,3 +249,29 @@ def test_kv_products_past_position_2_32_store_nothing(heads):
     before = raw_of(dc.pool).clone()
     mp.kv_matmul_paged(t["hidden"], t["input_row_offsets"], t["weight"], cache_of(dc), case.layer_idx)
     assert same(raw_of(dc.pool), before)
+
+
+@pytest.mark.parametrize("at", [False, True])
+def test_latent_writes_of_more_than_2_27_tokens(at):
+    # rows of 8 columns; all but the first 16 tokens of the first request lie past its page table
+    T = (1 << 27) + 9
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.zeros((T, 8), dtype=torch.bfloat16, device="cuda")
+    x[:16] = torch.randn((16, 8), generator=g, device="cuda").to(torch.bfloat16)
+    x[-5:] = torch.randn((5, 8), generator=g, device="cuda").to(torch.bfloat16)
+    pool = torch.zeros((4, 1, 1, 16, 1, 8), dtype=torch.bfloat16, device="cuda")
+    cache = mp.PagedKVCache(pool, i32([[2], [1]], "cuda"), i32([0, 3], "cuda"))
+    gamma = torch.rand(8, generator=g, device="cuda") + 0.5
+    offsets = i32([0, T - 5, T], "cuda")
+    if at:
+        pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+        mp.mla_write_latent_paged_at(x, offsets, pos, gamma, 1e-6, None, 8, cache, 0)
+    else:
+        mp.mla_write_latent_paged(x, offsets, gamma, 1e-6, None, 8, cache, 0)
+    want = torch.zeros((4, 16, 8), dtype=torch.float64, device="cuda")
+    for page, slots, rows in ((2, slice(0, 16), x[:16]), (1, slice(3, 8), x[-5:])):
+        r = rows.double()
+        want[page, slots] = gamma.double() * r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-6)
+    got = pool[:, 0, 0, :, 0].double()
+    # binary32: the sum of 8 squares, a root and a division, three products; then one rounding
+    assert bool(((got - want).abs() <= want.abs() * (16 * U32 + HALF_BF16 * 1.001)).all())
