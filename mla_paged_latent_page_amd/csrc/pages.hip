@@ -195,14 +195,15 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(PageArgs a)
 __device__ inline uint32_t lane_of(uint32_t v, int k) { return (uint32_t)__builtin_amdgcn_readlane((int)v, k); }
 
 // Page and slot of position p of request b; no page if it has none.  (Always loads: two calls
-// side by side then wait once.)
+// side by side then wait once.)  A length and a token's index are 32 bits each, their sum is not.
 __device__ inline void slot_of(const PageArgs& a, uint32_t b, uint64_t p, uint32_t& page, uint32_t& slot)
 {
     const bool there = p < (uint64_t)a.max_pages * a.page_size;
-    const uint32_t q = there ? (uint32_t)p : 0u, lp = q / a.page_size;
+    const uint64_t q = there ? p : 0u;
+    const uint32_t lp = q >> 32 ? (uint32_t)(q / a.page_size) : (uint32_t)q / a.page_size;
     const uint32_t pg = a.page_table[(size_t)b * a.max_pages + lp];
     page = there && pg < a.num_pages ? pg : kNoPage;
-    slot = q - lp * a.page_size;
+    slot = (uint32_t)q - lp * a.page_size;
 }
 
 // A wave owns 64 16-byte columns (or scales) of one request, layer and kv half and moves them

@@ -275,3 +275,22 @@ def test_latent_writes_of_more_than_2_27_tokens(at):
     got = pool[:, 0, 0, :, 0].double()
     # binary32: the sum of 8 squares, a root and a division, three products; then one rounding
     assert bool(((got - want).abs() <= want.abs() * (16 * U32 + HALF_BF16 * 1.001)).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_compaction_past_position_2_32(dtype):
+    # a length close to 2^32 in a table that reaches past it
+    ps, pages, D = 1 << 20, 3, 16
+    raw = torch.randint(0, 256, (pages, 1, 1, ps, 1, D * (1 if dtype == "e4m3" else 2)), dtype=torch.uint8, device="cuda")
+    pool = raw if dtype == "e4m3" else raw.view(torch.bfloat16)
+    scales = torch.rand((pages, 1, 1, ps, 1), device="cuda") if dtype == "e4m3" else None
+    table = torch.full((1, 4098), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, 4095], table[0, 4096] = 0, 1, 2
+    cache = mp.PagedKVCache(pool, table, i32([2 ** 32 - 5], "cuda"), scales=scales)
+    accepted = [2, 9, 0xFFFFFFFF]       # positions 2^32 - 3, 2^32 + 4 and one past the table
+    tensors = [raw_of(pool)] + ([] if scales is None else [scales])
+    want = [t.clone() for t in tensors]
+    for w, t in zip(want, tensors):
+        w[1, 0, 0, ps - 5], w[1, 0, 0, ps - 4] = t[1, 0, 0, ps - 3], t[2, 0, 0, 4]
+    mp.mla_compact_paged(i32(accepted, "cuda"), i32([0, 3], "cuda"), cache)
+    assert all(same(w, t) for w, t in zip(want, tensors))
