@@ -33,6 +33,7 @@
 // matrix cores align the 64 terms of such a product to about 13 bits below the largest (probed:
 // errors of 1.5e-4 of the sum of magnitudes), so it is not used.
 #include <algorithm>
+#include <cmath>
 #include <utility>
 
 #include "step.hpp"
@@ -1374,7 +1375,9 @@ __global__ void __launch_bounds__(256) tree_attention_join(MfmaParams P)
 
 bool tree_attention_mfma_fits(const TreeAttentionArgs& a, AttnKind kind)
 {
-    return (kind == ATTN_BF16 || kind == ATTN_E4M3) && a.scale != 0.0f && a.D == D && a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
+    // (the kernel's scale is in units of log2)
+    return (kind == ATTN_BF16 || kind == ATTN_E4M3) && a.scale != 0.0f && std::isfinite(a.scale * kLog2e) && a.D == D &&
+           a.K == K && a.L.stride_token < (int64_t(1) << 28) &&
            (kind == ATTN_BF16 || a.Ls.stride_token < (int64_t(1) << 28)) &&
            (uint64_t)a.L.batch * a.L.max_pages < (uint64_t(1) << 32) &&
            // items (at most one partly filled per request) times units

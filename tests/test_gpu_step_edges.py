@@ -294,3 +294,17 @@ def test_compaction_past_position_2_32(dtype):
         w[1, 0, 0, ps - 5], w[1, 0, 0, ps - 4] = t[1, 0, 0, ps - 3], t[2, 0, 0, 4]
     mp.mla_compact_paged(i32(accepted, "cuda"), i32([0, 3], "cuda"), cache)
     assert all(same(w, t) for w, t in zip(want, tensors))
+
+
+# ---------------------------------------------------------------------------
+# scales and scores at the ends of binary32
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", [16, 128])
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_a_scale_close_to_the_largest_number(scale, heads, dtype):
+    # queries of zero: every score is 0, the output the mean
+    case = AttentionCase(9, [200, 33], [2, 3], heads, mask="tree", dtype=dtype)
+    case.q.zero_()
+    case.scale = scale
+    check_attention(case, *attend(case))
