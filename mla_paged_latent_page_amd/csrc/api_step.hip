@@ -83,7 +83,7 @@ MLA_API mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t fir
         }
         a.quarters[j] = f / (kPi / 2);
         // No angle of 2^50 quarter turns: two bits of it would be left.
-        if (!(a.quarters[j] * ((double)first_position + rows) < 0x1p50))
+        if (!(a.quarters[j] * ((double)first_position + (rows - 1)) < 0x1p50))
             return MLA_ERR_INVALID_SHAPE;
     }
     if (mla_status_t st = check_device())
