@@ -790,7 +790,7 @@ mla_status_t mla_fork_paged(const uint32_t* parents, const uint32_t* children, c
  * ref_counts      [device] uint32 [num_pages], updated; counts below 2^31
  * free_list       [device] uint32 [num_pages], entries from free_count[0] on are written
  * free_count      [device] uint32 [1], updated
- * cache           page_table and cache_lengths are WRITTEN; blocks may be NULL
+ * cache           num_pages < 2^31; page_table and cache_lengths are WRITTEN; blocks may be NULL
  */
 mla_status_t mla_free_paged(const uint32_t* requests, int32_t count, uint32_t* ref_counts, uint32_t* free_list,
                             uint32_t* free_count, const mla_paged_cache_t* cache, void* stream);

@@ -429,7 +429,7 @@ MLA_API mla_status_t mla_free_paged(const uint32_t* requests, int32_t count, uin
     if (mla_status_t st = page_call(cache, nullptr, count, requests && ref_counts && free_list && free_count, false,
                                     true, a))
         return st;
-    if (count > 65536)
+    if (count > 65536 || (int64_t)cache->num_pages >= k2G)
         return MLA_ERR_INVALID_SHAPE;
     if (count == 0)
         return MLA_OK;

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(256) free_requests_kernel(PageArgs a)
 }
 
 // One block walks the counts in order, 16 per thread and step, and appends the marked
-// pages: the list does not depend on the order in which the references went.
+// pages: the list does not depend on the order in which the references went.  (num_pages is
+// below 2^31: neither the walk nor the sums wrap.)
 constexpr int COLLECT_THREADS = 1024, COLLECT_EACH = 16;
 __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(PageArgs a)
 {
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(COLLECT_THREADS) collect_kernel(PageArgs a)
                 a.free_list[at] = pg;
             ++at;
         }
-        base += all;   // at most the marks of num_pages pages: no wrap
+        base += all;
         __syncthreads();
     }
     if (threadIdx.x == 0)
