@@ -738,7 +738,7 @@ mla_status_t mla_tree_attention_paged_fp8_cache(const void* q_latent, const uint
  * and kv halves at once.  The four calls take any cache this library knows (BF16, F32, or
  * F8E4M3FN with cache_scales; cache_scales is NULL for the others); all copies are bit
  * copies, of the scales too.  Which page is free is the cache owner's bookkeeping: page ids
- * are handed in, and freed ones handed back in a list.
+ * are handed in, and freed ones handed back in a list.  Counts are at most 2^30.
  *
  * mla_copy_pages: page dst_pages[i] becomes a copy of page src_pages[i], i < count.
  *   No destination may be the source of another pair or appear twice.  Pairs with an id

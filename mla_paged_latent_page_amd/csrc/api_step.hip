@@ -12,6 +12,7 @@ using namespace mla;
 namespace {
 
 constexpr int64_t k2G = int64_t(1) << 31;
+constexpr int32_t kMostPagePairs = int32_t(1) << 30;   // a launch's worth below 2^31, in ints
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
@@ -337,7 +338,7 @@ mla_status_t page_call(const mla_paged_cache_t* cache, const mla_cache_scales_t*
     if (work && (!pointers || (blocks && !cache->blocks) || (lengths && (!cache->page_table || !cache->cache_lengths)) ||
                  (blocks && fp8 && !sc->scales)))
         return MLA_ERR_NULL_POINTER;
-    if (count < 0 || (cache->num_kv != 1 && cache->num_kv != 2))
+    if (count < 0 || count > kMostPagePairs || (cache->num_kv != 1 && cache->num_kv != 2))
         return MLA_ERR_INVALID_SHAPE;
     if (mla_status_t st = check_cache_shape(cache, cache->num_kv))
         return st;

@@ -20,3 +20,11 @@ def test_free_refuses_pools_whose_counts_its_walk_cannot_number(lib):  # noqa: F
     def free(pages):
         return lib.mla_free_paged(FAKE, 3, FAKE, FAKE, FAKE, ctypes.byref(cache_desc(pages=pages)), None)
     assert free(2 ** 31 - 1) == DEV and free(2 ** 31) == SHAPE and free(2 ** 32 - 1) == SHAPE
+
+
+def test_page_calls_refuse_counts_past_2_30(lib):  # noqa: F811
+    d = ctypes.byref(cache_desc())
+    for n, status in ((2 ** 30, DEV), (2 ** 30 + 1, SHAPE), (2 ** 31 - 1, SHAPE)):
+        assert lib.mla_copy_pages(FAKE, FAKE, n, d, None, None) == status
+        assert lib.mla_fork_paged(FAKE, FAKE, FAKE, n, FAKE, d, None, None) == status
+        assert lib.mla_compact_paged(FAKE, FAKE, n, d, None, None) == status
