@@ -308,3 +308,133 @@ def test_a_scale_close_to_the_largest_number(scale, heads, dtype):
     case.q.zero_()
     case.scale = scale
     check_attention(case, *attend(case))
+
+
+@pytest.mark.parametrize("length", ["capacity", "two less", "2^32 - 1", "2^31"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("heads, mask", [(16, "chain"), (16, "tree"), (64, "tree"), (128, "chain")])
+def test_attention_sees_the_positions_of_the_page_table(heads, mask, dtype, length):
+    """Request 0's length at and past what its table's row holds: the answer is that of the
+    positions below it alone."""
+    capacity, n = 112, 4
+    case = AttentionCase(heads, [capacity - n, 30], [n, 2], heads, mask=mask, dtype=dtype, page_size=16)
+    assert case.dev.page_table.shape[1] * 16 == capacity
+    cached = {"capacity": capacity, "two less": capacity - 2, "2^32 - 1": capacity, "2^31": capacity}[length]
+    word = {"capacity": capacity, "two less": capacity - 2, "2^32 - 1": 2 ** 32 - 1, "2^31": 2 ** 31}[length]
+    case.dev.cache_lengths.copy_(i32([word, 30], "cuda"))
+    got, z = attend(case)
+    # the reference: a request of `cached` rows whose drafted rows past the capacity nobody sees
+    rows = case.rows64(0)          # all positions below the capacity
+    kept = capacity - cached
+    case.lens = np.array([cached, 30])
+    case.seen[0] = [m & ((1 << kept) - 1) for m in case.seen[0]]
+    pad = torch.cat([rows, torch.zeros((cached + n - capacity, case.D), dtype=torch.float64, device="cuda")])
+    second = case.rows64(1)
+    case.rows64 = lambda b: second if b else pad
+    check_attention(case, got, z)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3", "f32"])
+@pytest.mark.parametrize("heads", [5, 24, 128])
+def test_outputs_at_large_scores(heads, dtype):
+    """Scores of several hundred: the bound of AttentionCase.reference with the weights' factor
+    exp(2 ds) written out (there it is taken to first order), nothing looser."""
+    case = AttentionCase(78 + heads, [700, 64], [5, 6], heads, mask="tree", q_std=40.0, dtype=dtype)
+    got, z = attend(case)
+    ref, zref, tol, ltol = case.reference()
+    at, extra = 0, torch.zeros_like(tol)
+    for b, n in enumerate(case.new.tolist()):
+        rows = case.rows64(b)
+        for i in range(n):
+            keep = [p for p in range(rows.shape[0]) if p < case.lens[b] or (case.seen[b][i] >> (p - int(case.lens[b]))) & 1]
+            r, q = rows[keep], case.q[at + i].double()
+            ds = ((q.abs() @ r.abs().t().contiguous()) * case.scale).amax(dim=1) * (case.D + 8) * U32
+            w = torch.softmax((q @ r.t().contiguous()) * case.scale, dim=1)
+            extra[at + i] = (w @ r[:, :case.K].abs()) * (torch.expm1(2 * ds) - 2 * ds)[:, None]
+        at += n
+    assert bool(((got.double() - ref).abs() <= tol + extra).all())
+    assert bool(((z.double() - zref).abs() <= ltol).all())
+
+
+# ---------------------------------------------------------------------------
+# a step captured and replayed
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_a_step_of_all_calls_captured_and_replayed(dtype):
+    """Free, fork, copy, rotate, write, attend and compact in one graph, replayed over changed inputs,
+    with eager calls between; every buffer as the eager calls leave it."""
+    H, ps, lens, new = 16, 16, [45, 130, 45, 0], [3, 5, 2, 0]
+    base = AttentionCase(31, lens[:3], new[:3], H, page_size=ps, mask="tree", dtype=dtype)
+    used = set(base.host.page_table.flatten().tolist())
+    spare = [p for p in range(base.host.num_pages) if p not in used]
+    assert len(spare) >= 2
+    table = np.full((4, base.host.page_table.shape[1]), 0xFFFFFFFF, np.int64)
+    table[:3] = base.host.page_table
+    refs = np.zeros(base.host.num_pages, np.int64)
+    for b in range(3):
+        refs[table[b, :-(-(lens[b] + new[b]) // ps)]] += 1
+    T = base.T
+    g = torch.Generator(device="cuda").manual_seed(4)
+    d = dict(pool=base.dev.pool.clone(), table=i32(table, "cuda"), lengths=i32(lens, "cuda"), refs=i32(refs, "cuda"),
+             list=torch.full((base.host.num_pages,), -1, dtype=torch.int32, device="cuda"), count=i32([0], "cuda"),
+             q=torch.zeros((T, H, 192), dtype=torch.bfloat16, device="cuda"),
+             out=torch.zeros((T, H, 512), dtype=torch.bfloat16, device="cuda"), lse=torch.zeros((T, H), device="cuda"),
+             freqs=torch.zeros((200, 64), device="cuda"))
+    if base.dev.scales is not None:
+        d["scales"] = base.dev.scales.clone()
+    cache = mp.PagedKVCache(d["pool"], d["table"], d["lengths"], scales=d.get("scales"))
+    iro = i32([0, 3, 8, 10, 10], "cuda")
+    pos = i32([45, 46, 46, 130, 131, 132, 131, 133, 45, 46], "cuda")
+    qin = torch.zeros_like(d["q"])
+    x = torch.zeros((T, 576), dtype=torch.bfloat16, device="cuda")
+    gamma = torch.rand(512, generator=g, device="cuda") + 0.5
+    ws = torch.empty(mp.mla_tree_attention_workspace_size(T, H, 512), dtype=torch.uint8, device="cuda")
+    ids = {k: i32(v, "cuda") for k, v in dict(gone=[3], parent=[0], child=[3], fresh=[spare[0]], src=[int(table[1, 0])],
+                                             dst=[spare[1]], accepted=[0, 2, 1, 4], offsets=[0, 2, 4, 4, 4]).items()}
+
+    def step():
+        d["count"].zero_()
+        mp.mla_free_paged(ids["gone"], d["refs"], d["list"], d["count"], cache)
+        mp.mla_fork_paged(ids["parent"], ids["child"], ids["fresh"], d["refs"], cache)
+        mp.mla_copy_pages(ids["src"], ids["dst"], cache)
+        mp.mla_rope_freqs(d["freqs"], scaling="linear", factor=2.0)
+        mp.mla_rope_q(qin, pos, d["freqs"], d["q"], layout="half")
+        write = mp.mla_write_latent_paged_fp8_at if dtype == "e4m3" else mp.mla_write_latent_paged_at
+        write(x, iro, pos, gamma, 1e-6, d["freqs"], 512, cache, 1, layout="half")
+        call = mp.mla_tree_attention_paged_fp8_cache if dtype == "e4m3" else mp.mla_tree_attention_paged
+        call(base.q, iro, base.mask, base.scale, 512, cache, 1, d["out"], ws, lse=d["lse"])
+        mp.mla_compact_paged(ids["accepted"], ids["offsets"], cache)
+
+    def fill(seed):
+        g.manual_seed(seed)
+        qin.copy_(torch.randn(qin.shape, generator=g, device="cuda"))
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+
+    def state():
+        torch.cuda.synchronize()
+        return {k: v.clone() for k, v in d.items()}
+
+    def put(s):
+        for k, v in s.items():
+            d[k].copy_(v)
+        torch.cuda.synchronize()
+    start = state()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    put(start)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(4):
+        fill(seed)
+        before = state()
+        graph.replay()
+        got = state()
+        put(before)
+        step()
+        want = state()
+        for k in want:
+            assert same(got[k].view(torch.uint8), want[k].view(torch.uint8)), (seed, k)
+        assert bool(torch.isfinite(want["out"].float()).all()) and int(want["lengths"][3]) == 45
