@@ -719,6 +719,9 @@ def mla_rope_freqs(freqs_cis, theta: float = 10000.0, first_position: int = 0, s
         raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, not {scaling!r}")
     if freqs_cis is None or freqs_cis.dim() != 2:
         raise ValueError("freqs_cis must be a [rows, d_rope] tensor")
+    for value, name in ((first_position, "first_position"), (original_max_position, "original_max_position")):
+        if not -2 ** 31 <= value < 2 ** 31:     # (other bits would be cut off)
+            raise ValueError(f"{name} must fit 32 bits, not {value}")
     rows, R = freqs_cis.shape
     fr = _f32(freqs_cis, "freqs_cis", rows * R)
     p = RopeParams(float(theta), float(factor), float(beta_fast), float(beta_slow), float(amplitude),

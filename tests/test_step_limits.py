@@ -3,6 +3,10 @@ are right stops at the device check."""
 import ctypes
 import math
 
+import pytest
+import torch
+
+import mla_paged_latent_page_amd as mp
 from test_step_host import DEV, FAKE, SHAPE, cache_desc, freqs, lib  # noqa: F401
 
 
@@ -28,3 +32,10 @@ def test_page_calls_refuse_counts_past_2_30(lib):  # noqa: F811
         assert lib.mla_copy_pages(FAKE, FAKE, n, d, None, None) == status
         assert lib.mla_fork_paged(FAKE, FAKE, FAKE, n, FAKE, d, None, None) == status
         assert lib.mla_compact_paged(FAKE, FAKE, n, d, None, None) == status
+
+
+@pytest.mark.parametrize("kw", [dict(first_position=2 ** 32), dict(first_position=2 ** 31),
+                                dict(original_max_position=2 ** 32 + 4096, scaling="by_parts")])
+def test_binding_refuses_positions_that_an_int32_would_cut_off(kw):
+    with pytest.raises(ValueError, match=next(iter(kw))):
+        mp.mla_rope_freqs(torch.zeros((4, 64)), **kw)
