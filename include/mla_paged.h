@@ -624,7 +624,7 @@ mla_status_t mla_rope_freqs(const mla_rope_params_t* params, int32_t first_posit
  *                 t * stride_token + h * stride_head (elements, one pair of strides each),
  *                 16-byte aligned, strides and d_nope multiples of 16 bytes.  q_out == q
  *                 with the same strides rotates in place and touches the rope columns only;
- *                 any other overlap is not allowed.
+ *                 any other overlap, also of q_out's rows with one another, is not allowed.
  * total_tokens    [host] T >= 0;  num_heads >= 1;  T * num_heads * (d_nope + d_rope) < 2^40
  * d_nope          0 <= d_nope <= 4096
  * d_rope          8 <= d_rope <= 512; % 8 == 0, and % 16 == 0 with MLA_ROPE_HALF
@@ -675,7 +675,8 @@ mla_status_t mla_write_latent_paged_fp8_at(const void* kv_input, const uint32_t*
  *   A token that sees no row gets zeros and an lse of -infinity.  Scores, the running
  *   maximum and sum, and the output sums are binary32; the weights exp(s_p - max) are
  *   rounded to bf16 for the product with the rows on bf16 and e4m3 caches.  out_latent is
- *   rounded once (round to nearest even).
+ *   rounded once (round to nearest even).  Scores are to stay below 2^30 in magnitude, where
+ *   binary32 still tells them apart by less than 2^7.
  *
  * What a row that a token does not see holds (NaN and infinities included) does not change
  * that token's output; neither does anything behind a request's last drafted row.
@@ -719,6 +720,7 @@ mla_status_t mla_tree_attention_paged(const void* q_latent, const uint32_t* inpu
  * columns.  The codes go into the products as they are (bf16 holds every e4m3 value); the
  * scales multiply the scores' block sums and the weights, in binary32 (an infinite scale
  * thus makes a block's sum infinite, and its 128 columns NaN for the tokens that see the row).
+ * Shapes off the matrix cores multiply the codes by the scales first.
  *
  * q_latent, out_latent  bf16
  * cache           dtype F8E4M3FN, D_c % 16 == 0

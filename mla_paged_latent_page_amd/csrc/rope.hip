@@ -14,7 +14,7 @@
 // pairs of the rope part for every head it visits, so the token's (cos, sin) row is
 // read once into registers.  Bound by memory: the nope columns are only copied, in
 // 16-byte pieces that are all in flight before the first store.  8,300 tokens of 128
-// heads: 156 us, 5.2 TB/s of reads and writes; 83 tokens of 16 heads: 3 us.
+// heads: 158 us, 5.2 TB/s of reads and writes; 83 tokens of 16 heads: 3 us.
 #include <algorithm>
 
 #include "step.hpp"

@@ -7,28 +7,42 @@
 // throughout: its maximum, sum and rescaling need no exchange but one swap of the wave's halves,
 // and P goes from the score layout into the next product's operand as it is.  The 32 x 512
 // output sums are the wave's 256 accumulation registers, so there is one wave per SIMD, and
-// everything else fits around them: the scores of tile t + 1 are computed while the weights of
-// tile t are, the loads of tile t + 3 go into a four-stage LDS ring in between.  The reference
-// is the running maximum, let lag by up to 2^8 (the weights stay below 2^8 in binary32), so the
-// sums are rescaled only now and then.  Weights are rounded to bf16 for the product, their sum
-// is not.
+// everything else has the 256 ordinary ones: the scores of tile t + 1 are computed while the weights
+// of tile t are, the loads of tile t + 3 go into a four-stage LDS ring in between.  They do not
+// quite suffice: 74 to 102 values per variant are spilled (284 to 368 bytes a lane), most of them
+// before the first step and around the join of two pairs.  Inside the steps, sixteen are reloaded
+// for each tile that has to be masked (the bits of its rows; every reload also waits for the loads
+// in flight), and constants that come back in the first step put a wait into all of them.  The
+// reference is the running maximum, let lag by up to 2^8 (the weights stay below 2^8 in binary32),
+// so the sums are rescaled only now and then.  Weights are rounded to bf16 for the product, their
+// sum is not.
 //
 // Work: every workgroup takes an equal share of all tiles of all requests (one workgroup per
 // CU); shares that end inside an item leave their sums, maximum and sum in the workspace in
 // binary32, and tree_attention_join adds them up in a fixed order.  Requests with few query rows
 // take narrower items, whose cache rows two pairs of waves share (Shape).
 //
-// Measured (MI355X, main kernel + join):
-//   12 requests of 17-33 tokens x 128 heads, 1300-6000 rows, bf16: 250-285 + 26 us, 860 TFLOP/s.
-//     Bound by the matrix cores (52 % busy) and by what a single wave per SIMD can issue between
-//     their instructions, at the clock the power limit leaves.
-//   64 requests of one token x 128 heads, 256-4096 rows, bf16: 50 + 12 us.  Bound by memory and its
-//     latency: the rows, the queries of every share, and the partial results, written and read.
-//   5 requests of 5-8 tokens x 16 heads, 78-94 thousand rows, e4m3: 150-185 + 11 us.  Bound by
-//     instruction issue: each wave converts every tile's codes to bf16 (272 conversions next to
+// Measured (MI355X; kernel trace, mean of 25 calls with their range, main kernel + join; then the
+// calls back to back):
+//   12 requests of 17-33 tokens x 128 heads, 1300-6000 rows, bf16: 272 (243-292) + 26 us; 260 us, 897
+//     TFLOP/s.  Bound by the matrix cores (53 % busy) and by what a single wave per SIMD can issue
+//     between their instructions, at the clock the power limit leaves.
+//   64 requests of one token x 128 heads, 256-4096 rows, bf16: 52 (51-66) + 12 us; 70 us with rows from
+//     memory.  Bound by memory: 140 MB read and 66 MB written by the main kernel, 39 MB read by the join.
+//     About 90 MB of it are partial results, written and read again; fewer, larger shares side by side
+//     would leave fewer.
+//   5 requests of 5-8 tokens x 16 heads, 78-94 thousand rows, e4m3: 181 (172-190) + 11 us; 163 us.  Bound
+//     by instruction issue: each wave converts every tile's codes to bf16 (272 conversions next to
 //     68 products); 80-128 of an item's 128 rows hold queries.
 //   4 requests of one token x 16 heads, 100-600 rows, bf16: 15 + 6 us, a chain of loads
 //     (offsets, page ids, rows) and two launches.
+//   Page sizes that are no multiple of 8 look up a page id per lane in every step, which waits for the
+//     loads in flight: 100 against 64 tokens, the cases above with bf16 / e4m3 rows: trees 269 against
+//     268 / 345 against 322 us, 64 requests 67 against 63 / 81 against 74, long contexts 190 against
+//     164 / 209 against 164.
+//   A chain is multiplied in full, hidden tiles included, and every tile of its own tokens is masked: a
+//     prompt chunk of 2048 tokens x 128 heads 2.3 ms (bf16) and 1.9 ms (e4m3), behind 4096 rows 4.0 and
+//     4.2 ms.
 // An e4m3 product with the queries split into two e4m3 parts would need no conversion, but the
 // matrix cores align the 64 terms of such a product to about 13 bits below the largest (probed:
 // errors of 1.5e-4 of the sum of magnitudes), so it is not used.
