@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(64 * WRITE_WAVES) latent_write_kernel(typename
         if constexpr (AT)
             pr = a.pos[t];
         const uint32_t pf = pr < (uint32_t)a.max_seq ? pr : (uint32_t)a.max_seq - 1;   // freqs row, clamped
-        // -1: no slot for this position (or it is past 2^32), nothing is stored
-        off[k] = p < first ? -1 : store_offset(a.L, b, p);
+        // -1: no slot for this position, nothing is stored; nor is it past 2^32 (behind the page's load:
+        // a branch before it made the e4m3 write 43.3 us of 42.0, the bf16 one 37.8 of 37.2)
+        off[k] = store_offset(a.L, b, p) | -(int64_t)(p < first);
         soff[k] = FP8 ? store_offset(a.Ls, b, p) : 0;
         const float* f = a.freqs + (int64_t)pf * a.R + pair0 * 2;
         fr0[k] = rot ? *reinterpret_cast<const f32x4*>(f) : f32x4{0.f, 0.f, 0.f, 0.f};
