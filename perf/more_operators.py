@@ -368,12 +368,11 @@ def _write_plain(s):
             width = KH * D
             x = torch.nn.functional.pad(x.reshape(m, width), (0, -width % BLOCK)).view(m, -1, BLOCK)
             top = x.abs().amax(dim=2)
-            zero = top == 0
-            safe = torch.where(zero, torch.ones_like(top), top)
-            codes = x * torch.where(zero, torch.ones_like(top), CODES_MAX / safe)[..., None]
-            codes = codes.view(m, -1)[:, :width].to(torch.float8_e4m3fn).view(torch.uint8).view(m, KH, D)
-            s["pool"].view(torch.uint8)[page, 0, half, slot] = codes
-            s["scales"][page, 0, half, slot] = torch.where(zero, torch.ones_like(top), top / CODES_MAX)
+            most = torch.full_like(top, CODES_MAX)     # (by a number, torch multiplies by its reciprocal)
+            safe = torch.where(top == 0, most, top)
+            codes = (x * (most / safe)[..., None]).view(m, -1)[:, :width].to(torch.float8_e4m3fn)
+            s["pool"].view(torch.uint8)[page, 0, half, slot] = codes.view(torch.uint8).view(m, KH, D)
+            s["scales"][page, 0, half, slot] = safe / most
     return s["pool"] if s["scales"] is None else (s["pool"], s["scales"])
 
 
