@@ -37,7 +37,7 @@
  *     id, page index and row to the buffers they were given, so a bad index
  *     yields unspecified values in the output rows it affects but never an
  *     access outside the pool, the weight or the outputs.  Write paths
- *     (kv_matmul_paged, mla_write_latent_paged(_fp8)(_at)) store nothing for a token
+ *     (kv_matmul_paged, kv_write_paged(_fp8), mla_write_latent_paged(_fp8)(_at)) store nothing for a token
  *     whose position lies past its request's page table or whose page id lies
  *     past the pool; every other byte of the pool keeps its value.
  *   - Shapes whose 256-row tiles would need byte offsets of 2^31 or more (a
@@ -815,6 +815,141 @@ mla_status_t mla_free_paged(const uint32_t* requests, int32_t count, uint32_t* r
 mla_status_t mla_compact_paged(const uint32_t* accepted, const uint32_t* accepted_offsets, int32_t total_accepted,
                                const mla_paged_cache_t* cache, const mla_cache_scales_t* cache_scales,
                                void* stream);
+
+/*
+ * Operators over the paged K/V cache (num_kv == 2, the cache that kv_matmul_paged fills):
+ * writes of keys and values that exist already, attention, and reading rows back.  The
+ * layout of a cached key's columns is that of the latent rows: each head's last d_rope
+ * columns are the rotated ones (d_nope = head_dim - d_rope in mla_rope_q, for the queries).
+ *
+ * kv_write_paged: token t of request b goes to position p = cache_lengths[b] +
+ * (t - input_row_offsets[b]), as with kv_matmul_paged:
+ *   K row[h*head_dim + c] = bf16(k[t][h][c]),                     c < head_dim - d_rope
+ *                         = bf16(k[t][h][c] rotated with freqs_cis[positions[t]]), the others
+ *   V row[h*head_dim + c] = bf16(v[t][h][c])
+ *   in binary32, round to nearest even; pairs and tables as in mla_rope_q.  No other byte of
+ *   the pool is written, cache_lengths is not updated, and tokens without a slot are skipped.
+ *
+ * k, v            [device] bf16 [total_tokens][num_heads][head_dim], token t at t * stride
+ *                 elements (views into a fused projection are taken as they are); 16-byte
+ *                 aligned, strides multiples of 8 elements, >= num_heads*head_dim
+ * input_row_offsets [device] uint32 [batch_size+1], [0] = 0, nondecreasing
+ * total_tokens    [host] input_row_offsets[batch_size]
+ * positions       [device] uint32 [total_tokens]: the freqs_cis row of each token; NULL: the
+ *                 position it is written to.  Past the table: its last row
+ * freqs_cis       [device] float [max_seq_len][d_rope], 16-byte aligned; may be NULL when
+ *                 d_rope == 0
+ * d_rope          0 <= d_rope <= head_dim, % 8 == 0, and % 16 == 0 with MLA_ROPE_HALF
+ * rope_layout     mla_rope_layout_t
+ * cache           [host] BF16, num_kv == 2, head_dim % 8 == 0, num_heads*head_dim <= 2^20, cache_lengths
+ *                 set; pages are WRITTEN
+ */
+mla_status_t kv_write_paged(const void* k, const void* v, int64_t k_stride_token, int64_t v_stride_token,
+                            const uint32_t* input_row_offsets, int32_t total_tokens, const uint32_t* positions,
+                            const float* freqs_cis, int32_t max_seq_len, int32_t d_rope, int32_t rope_layout,
+                            const mla_paged_cache_t* cache, uint32_t layer_idx, void* stream);
+
+/*
+ * kv_write_paged into an e4m3 cache: the same values in binary32, quantised per block of 128
+ * columns of the K row and of the V row:
+ *   amax = max |y| of the block, s = amax / 448 (1 for a block of zeros)
+ *   codes = e4m3fn(y * (448 / amax)), round to nearest even; s into the scale pool
+ * An amax below 448 * 2^-126 counts as that.
+ *
+ * cache           dtype F8E4M3FN, num_heads*head_dim % 16 == 0; pages are WRITTEN
+ * cache_scales    [host] granularity 128, stride_token >= ceil(num_heads*head_dim / 128),
+ *                 stride_kv >= that; WRITTEN
+ */
+mla_status_t kv_write_paged_fp8(const void* k, const void* v, int64_t k_stride_token, int64_t v_stride_token,
+                                const uint32_t* input_row_offsets, int32_t total_tokens, const uint32_t* positions,
+                                const float* freqs_cis, int32_t max_seq_len, int32_t d_rope, int32_t rope_layout,
+                                const mla_paged_cache_t* cache, const mla_cache_scales_t* cache_scales,
+                                uint32_t layer_idx, void* stream);
+
+/*
+ * Read rows of the K/V cache back into contiguous buffers (the gather of
+ * mla_gather_latent_paged for both halves):
+ *   k_buffer[r], v_buffer[r] = K and V row of token cache_offsets[b] + i of request b,
+ *   r = buffer_row_offsets[b] + i;  a bit copy, or from an e4m3 cache
+ *   bf16(code * scale of its block of 128 columns), round to nearest even.
+ *
+ * buffer_row_offsets, cache_offsets, buffer_length  as in mla_decompress_k_paged
+ * cache           num_kv == 2; BF16 or F32 (kv_gather_paged), F8E4M3FN (kv_gather_paged_fp8_cache);
+ *                 num_heads*head_dim <= 2^20
+ * k_buffer, v_buffer  [device] [>= buffer_length][num_heads*head_dim], the cache's dtype or
+ *                 bf16 (e4m3 cache); 16-byte aligned, written
+ */
+mla_status_t kv_gather_paged(const uint32_t* buffer_row_offsets, const uint32_t* cache_offsets,
+                             int32_t buffer_length, const mla_paged_cache_t* cache, uint32_t layer_idx,
+                             void* k_buffer, void* v_buffer, void* stream);
+mla_status_t kv_gather_paged_fp8_cache(const uint32_t* buffer_row_offsets, const uint32_t* cache_offsets,
+                                       int32_t buffer_length, const mla_paged_cache_t* cache,
+                                       const mla_cache_scales_t* cache_scales, uint32_t layer_idx,
+                                       void* k_buffer, void* v_buffer, void* stream);
+
+/*
+ * Attention of new tokens over the paged K/V cache: chunks of a prompt, single tokens, or
+ * both in one batch.  The new tokens' own rows are in the cache already (kv_matmul_paged or
+ * kv_write_paged, with the same cache_lengths).
+ *
+ *   Token i of request b (t = input_row_offsets[b] + i) is at position p = cache_lengths[b] + i.
+ *   It sees the rows at positions k <= p; with a window, of these only those with
+ *   p - k < window or k < sinks.  Query head h reads key head h / (num_heads / cache->num_heads):
+ *     s_k          = scale * sum_c q[t][h][c] * K_k[c]             (k seen)
+ *     out[t][h][c] = sum_k exp(s_k) * V_k[c] / sum_k exp(s_k)
+ *     lse[t][h]    = ln sum_k exp(s_k)
+ *   A token that sees no row (its window lies past the page table) gets zeros and an lse of
+ *   -infinity.  Scores, the running maximum and sum, and the output sums are binary32; the
+ *   weights are rounded to bf16 for the product with V where the matrix cores do it.  out is
+ *   rounded once (round to nearest even).  Scores are to stay below 2^30 in magnitude.
+ *
+ * What a row that a token does not see holds (NaN and infinities included) does not change
+ * that token's output, nor does anything behind a request's last new token.  Of the rows it
+ * does see, a score of NaN or +infinity makes the token's head NaN, lse included; a score of
+ * -infinity is a weight of 0, which makes NaN of the columns in which that V row is not finite.
+ *
+ * q               [device] [total_tokens][num_heads][head_dim], token t at t * q_stride_token
+ *                 elements; bf16 with a BF16 cache, float with an F32 cache; 16-byte aligned,
+ *                 the stride a multiple of 16 bytes and >= num_heads*head_dim
+ * input_row_offsets [device] uint32 [batch_size+1], [0] = 0, nondecreasing; rows of q, out and
+ *                 lse at or past input_row_offsets[batch_size] are neither read nor written to.
+ *                 Where they do decrease the outputs are unspecified.
+ * total_tokens    [host] T >= input_row_offsets[batch_size]
+ * num_heads       a multiple of cache->num_heads; T * num_heads < 2^31 - 2^16
+ * scale           finite, |scale| below 2^127
+ * window          0: none; else the rows a token sees, its own included
+ * sinks           first rows that stay visible behind a window (without one: no effect)
+ * cache           [host] num_kv == 2, BF16 or F32, head_dim % 8 == 0, head_dim <= 256, cache_lengths
+ *                 set and below 2^31.  Positions past the page table (max_pages_per_seq * page_size) are not
+ *                 seen; that product < 2^31.
+ * out             [device] [total_tokens][num_heads][head_dim] in q's dtype, 16-byte aligned, written
+ * lse             [device] float [total_tokens][num_heads], 4-byte aligned, written; or NULL
+ * workspace       [device] >= kv_attention_workspace_size(T, num_heads, cache->num_heads,
+ *                 head_dim) bytes, 256-byte aligned.  Nothing in it has to start at zero.  Calls
+ *                 that may overlap (other streams, captured graphs replayed side by side) need
+ *                 workspaces of their own.
+ * Heads of 64 and of 128 columns on BF16 and e4m3 caches run on the matrix cores.
+ */
+size_t kv_attention_workspace_size(int32_t total_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
+mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uint32_t* input_row_offsets,
+                                int32_t total_tokens, int32_t num_heads, float scale, int32_t window, int32_t sinks,
+                                const mla_paged_cache_t* cache, uint32_t layer_idx, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kv_attention_paged on an e4m3 cache: K_k[c] and V_k[c] = code * scale of the block of 128
+ * columns of the token row that holds the column.
+ *
+ * q, out          bf16
+ * cache           dtype F8E4M3FN
+ * cache_scales    [host] granularity 128, stride_token >= ceil(cache->num_heads*head_dim / 128)
+ * Other arguments, limits and errors as in kv_attention_paged.
+ */
+mla_status_t kv_attention_paged_fp8_cache(const void* q, int64_t q_stride_token, const uint32_t* input_row_offsets,
+                                          int32_t total_tokens, int32_t num_heads, float scale, int32_t window,
+                                          int32_t sinks, const mla_paged_cache_t* cache,
+                                          const mla_cache_scales_t* cache_scales, uint32_t layer_idx, void* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* mla_status_string(mla_status_t status);

@@ -21,6 +21,9 @@ Entry points (same names as the C ABI):
   mla_write_latent_paged(_fp8)_at  the latent writes with the rope position of each token given
   mla_tree_attention_paged(_fp8_cache)  attention of absorbed queries over cached and drafted rows
   mla_copy_pages, mla_fork_paged, mla_free_paged, mla_compact_paged  page upkeep
+  kv_write_paged(_fp8)         keys (rotated) and values of new tokens into K/V cache pages
+  kv_gather_paged(_fp8_cache)  rows of a K/V cache into contiguous buffers
+  kv_attention_paged(_fp8_cache)  causal attention of new tokens over a K/V cache, with or without a window
   mla_check_indices            debug validation of index arrays (synchronous)
 """
 from __future__ import annotations
@@ -47,7 +50,9 @@ EXPORTS = ("mla_paged_cache_default_strides", "mla_decompress_k_paged", "mla_gat
            "mla_write_latent_paged_fp8", "mla_decompress_kv_paged_fp8_cache", "mla_decompress_k_paged_fp8_noalloc",
            "mla_rope_freqs", "mla_rope_q", "mla_write_latent_paged_at", "mla_write_latent_paged_fp8_at",
            "mla_tree_attention_workspace_size", "mla_tree_attention_paged", "mla_tree_attention_paged_fp8_cache",
-           "mla_copy_pages", "mla_fork_paged", "mla_free_paged", "mla_compact_paged")
+           "mla_copy_pages", "mla_fork_paged", "mla_free_paged", "mla_compact_paged",
+           "kv_write_paged", "kv_write_paged_fp8", "kv_gather_paged", "kv_gather_paged_fp8_cache",
+           "kv_attention_workspace_size", "kv_attention_paged", "kv_attention_paged_fp8_cache")
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "by_parts": 2}
 # mla_decompress_k_paged_fp8_noalloc's fixed device array (include/mla_paged.h)
@@ -169,6 +174,21 @@ def lib():
             L.mla_free_paged.restype = i32
             L.mla_compact_paged.argtypes = [vp, vp, i32, cd, sd, vp]
             L.mla_compact_paged.restype = i32
+            L.kv_write_paged.argtypes = [vp, vp, i64, i64, vp, i32, vp, vp, i32, i32, i32, cd, u32, vp]
+            L.kv_write_paged.restype = i32
+            L.kv_write_paged_fp8.argtypes = [vp, vp, i64, i64, vp, i32, vp, vp, i32, i32, i32, cd, sd, u32, vp]
+            L.kv_write_paged_fp8.restype = i32
+            L.kv_gather_paged.argtypes = [vp, vp, i32, cd, u32, vp, vp, vp]
+            L.kv_gather_paged.restype = i32
+            L.kv_gather_paged_fp8_cache.argtypes = [vp, vp, i32, cd, sd, u32, vp, vp, vp]
+            L.kv_gather_paged_fp8_cache.restype = i32
+            L.kv_attention_workspace_size.argtypes = [i32, i32, i32, i32]
+            L.kv_attention_workspace_size.restype = sz
+            L.kv_attention_paged.argtypes = [vp, i64, vp, i32, i32, f32, i32, i32, cd, u32, vp, vp, vp, sz, vp]
+            L.kv_attention_paged.restype = i32
+            L.kv_attention_paged_fp8_cache.argtypes = [vp, i64, vp, i32, i32, f32, i32, i32, cd, sd, u32, vp, vp, vp, sz,
+                                                       vp]
+            L.kv_attention_paged_fp8_cache.restype = i32
             L.kv_matmul_paged.argtypes = [vp, vp, i32, i32, vp, ctypes.POINTER(CacheDesc), u32, vp]
             L.kv_matmul_paged.restype = i32
             L.mla_gather_latent_paged.argtypes = [vp, vp, i32, ctypes.POINTER(CacheDesc), u32, vp, vp]
@@ -921,6 +941,137 @@ def mla_compact_paged(accepted, accepted_offsets, cache: PagedKVCache, stream=No
     _gpu(accepted=accepted, accepted_offsets=accepted_offsets, cache=cache)
     st = lib().mla_compact_paged(acc, off, accepted.numel(), ctypes.byref(desc), sdesc, _stream(stream))
     _check(st, "mla_compact_paged")
+
+
+def _heads(t, what, tokens, heads, head_dim, dtype):
+    """A [tokens, heads, head_dim] tensor or view whose heads are contiguous; its pointer and token stride."""
+    if t is None or t.dim() != 3 or tuple(t.shape) != (tokens, heads, head_dim):
+        raise ValueError(f"{what} must be a [{tokens}, {heads}, {head_dim}] tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be of dtype {dtype}, not {t.dtype}")
+    if t.stride(2) != 1 and head_dim > 1 or heads > 1 and t.stride(1) != head_dim:
+        raise ValueError(f"the heads of a token of {what} must be contiguous")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * head_dim
+
+
+def _kv_write(k, v, input_row_offsets, cache, layer_idx, positions, freqs_cis, layout, stream, fp8):
+    import torch
+    name = "kv_write_paged_fp8" if fp8 else "kv_write_paged"
+    desc, sdesc = _cache_desc(cache, scales=True) if fp8 else (_cache_desc(cache), None)
+    if k is None or k.dim() != 3:
+        raise ValueError("k must be a [T, heads, head_dim] tensor")
+    T, H, D = k.shape[0], desc.num_heads, desc.head_dim
+    kp, ks = _heads(k, "k", T, H, D, torch.bfloat16)
+    vp, vs = _heads(v, "v", T, H, D, torch.bfloat16)
+    iro = _u32(input_row_offsets, "input_row_offsets", desc.batch_size + 1)
+    pos = None if positions is None else _u32(positions, "positions", T)
+    lay = _rope_layout(layout)
+    fr, rope, max_seq = None, 0, 0
+    if freqs_cis is not None:
+        fr = _freqs(freqs_cis)
+        max_seq, rope = freqs_cis.shape
+    _gpu(k=k, v=v, input_row_offsets=input_row_offsets, positions=positions, freqs_cis=freqs_cis, cache=cache)
+    args = (kp, vp, ks, vs, iro, T, pos, fr, max_seq, rope, lay, ctypes.byref(desc))
+    if fp8:
+        st = lib().kv_write_paged_fp8(*args, ctypes.byref(sdesc), int(layer_idx), _stream(stream))
+    else:
+        st = lib().kv_write_paged(*args, int(layer_idx), _stream(stream))
+    _check(st, name)
+
+
+def kv_write_paged(k, v, input_row_offsets, cache: PagedKVCache, layer_idx: int, positions=None, freqs_cis=None,
+                   layout: str = "interleaved", stream=None) -> None:
+    """Place keys and values ([T, heads, head_dim] bfloat16, views with contiguous heads are taken as they
+    are) behind the cached rows of each request.  With freqs_cis ([max_seq_len, d_rope]) the last d_rope
+    columns of every key head are rotated at positions (None: the position written to)."""
+    _kv_write(k, v, input_row_offsets, cache, layer_idx, positions, freqs_cis, layout, stream, False)
+
+
+def kv_write_paged_fp8(k, v, input_row_offsets, cache: PagedKVCache, layer_idx: int, positions=None, freqs_cis=None,
+                       layout: str = "interleaved", stream=None) -> None:
+    """kv_write_paged into an e4m3 cache: codes with a scale per 128 columns of the token row."""
+    _kv_write(k, v, input_row_offsets, cache, layer_idx, positions, freqs_cis, layout, stream, True)
+
+
+def _kv_gather(buffer_row_offsets, cache_offsets, buffer_length, cache, layer_idx, k_buffer, v_buffer, stream, fp8):
+    desc, sdesc = _cache_desc(cache, scales=True) if fp8 else (_cache_desc(cache), None)
+    M, HD = int(buffer_length), desc.num_heads * desc.head_dim
+    dtypes = _dtypes()[MLA_DTYPE_BF16] if fp8 else _dtypes().get(desc.dtype)
+    nbytes = M * HD * (2 if fp8 else _bytes_of(desc.dtype))
+    kb, vb = _buf(k_buffer, "k_buffer", nbytes, dtypes), _buf(v_buffer, "v_buffer", nbytes, dtypes)
+    bro, co = _index_args(buffer_row_offsets, cache_offsets, desc)
+    _gpu(buffer_row_offsets=buffer_row_offsets, cache_offsets=cache_offsets, k_buffer=k_buffer, v_buffer=v_buffer,
+         cache=cache)
+    if fp8:
+        st = lib().kv_gather_paged_fp8_cache(bro, co, M, ctypes.byref(desc), ctypes.byref(sdesc), int(layer_idx), kb,
+                                             vb, _stream(stream))
+        _check(st, "kv_gather_paged_fp8_cache")
+    else:
+        st = lib().kv_gather_paged(bro, co, M, ctypes.byref(desc), int(layer_idx), kb, vb, _stream(stream))
+        _check(st, "kv_gather_paged")
+
+
+def kv_gather_paged(buffer_row_offsets, cache_offsets, buffer_length: int, cache: PagedKVCache, layer_idx: int,
+                    k_buffer, v_buffer, stream=None) -> None:
+    """k_buffer[r], v_buffer[r] = key and value row of a K/V cache (a bit copy)."""
+    _kv_gather(buffer_row_offsets, cache_offsets, buffer_length, cache, layer_idx, k_buffer, v_buffer, stream, False)
+
+
+def kv_gather_paged_fp8_cache(buffer_row_offsets, cache_offsets, buffer_length: int, cache: PagedKVCache,
+                              layer_idx: int, k_buffer, v_buffer, stream=None) -> None:
+    """kv_gather_paged from an e4m3 cache: codes times their block scales, rounded to bfloat16."""
+    _kv_gather(buffer_row_offsets, cache_offsets, buffer_length, cache, layer_idx, k_buffer, v_buffer, stream, True)
+
+
+def kv_attention_workspace_size(total_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(lib().kv_attention_workspace_size(int(total_tokens), int(num_heads), int(num_kv_heads), int(head_dim)))
+
+
+def _kv_attention(q, input_row_offsets, scale, cache, layer_idx, out, workspace, window, sinks, lse, stream, fp8):
+    import torch
+    desc, sdesc = _cache_desc(cache, scales=True) if fp8 else (_cache_desc(cache), None)
+    dtype = torch.float32 if desc.dtype == MLA_DTYPE_F32 else torch.bfloat16
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be a [T, H, head_dim] tensor")
+    T, H, D = q.shape[0], q.shape[1], desc.head_dim
+    qp, qs = _heads(q, "q", T, H, D, dtype)
+    for value, what in ((window, "window"), (sinks, "sinks")):
+        if not 0 <= value < 2 ** 31:     # (other bits would be cut off)
+            raise ValueError(f"{what} must be at least 0 and fit 32 bits, not {value}")
+    if out is None or tuple(out.shape) != (T, H, D):
+        raise ValueError(f"out must be a [{T}, {H}, {D}] tensor")
+    op = _buf(out, "out", T * H * D * out.element_size(), (dtype,))
+    ls = None
+    if lse is not None:
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse must be a [{T}, {H}] tensor")
+        ls = _f32(lse, "lse", T * H)
+    iro = _u32(input_row_offsets, "input_row_offsets", desc.batch_size + 1)
+    ws, ws_bytes = _workspace(workspace)
+    _gpu(q=q, input_row_offsets=input_row_offsets, out=out, lse=lse, workspace=workspace, cache=cache)
+    args = (qp, qs, iro, T, H, float(scale), int(window), int(sinks), ctypes.byref(desc))
+    if fp8:
+        st = lib().kv_attention_paged_fp8_cache(*args, ctypes.byref(sdesc), int(layer_idx), op, ls, ws, ws_bytes,
+                                                _stream(stream))
+        _check(st, "kv_attention_paged_fp8_cache")
+    else:
+        st = lib().kv_attention_paged(*args, int(layer_idx), op, ls, ws, ws_bytes, _stream(stream))
+        _check(st, "kv_attention_paged")
+
+
+def kv_attention_paged(q, input_row_offsets, scale: float, cache: PagedKVCache, layer_idx: int, out, workspace,
+                       window: int = 0, sinks: int = 0, lse=None, stream=None) -> None:
+    """out[t, h] = softmax(scale * q[t, h] . K) V over the rows of the token's request up to its own, of these
+    only the newest `window` and the first `sinks` where a window is given.  q: [T, H, head_dim], a view with
+    contiguous heads is taken as it is; lse: optional float32 [T, H].  ``workspace``: a device tensor of at
+    least kv_attention_workspace_size(T, H, cache heads, head_dim) bytes."""
+    _kv_attention(q, input_row_offsets, scale, cache, layer_idx, out, workspace, window, sinks, lse, stream, False)
+
+
+def kv_attention_paged_fp8_cache(q, input_row_offsets, scale: float, cache: PagedKVCache, layer_idx: int, out,
+                                 workspace, window: int = 0, sinks: int = 0, lse=None, stream=None) -> None:
+    """kv_attention_paged over an e4m3 cache (codes times their block scales)."""
+    _kv_attention(q, input_row_offsets, scale, cache, layer_idx, out, workspace, window, sinks, lse, stream, True)
 
 
 def status_string(status: int) -> str:
