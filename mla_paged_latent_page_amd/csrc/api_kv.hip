@@ -236,7 +236,8 @@ MLA_API size_t kv_attention_workspace_size(int32_t total_tokens, int32_t num_hea
     if (total_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads || head_dim <= 0 ||
         head_dim > 256)
         return 0;
-    return 256;
+    const size_t piece = (size_t)kv_attention_row_groups(total_tokens, num_heads / num_kv_heads) * 32 * (head_dim + 2);
+    return align256(2 * kKvGroups * piece * sizeof(float) + (kKvGroups + 1) * sizeof(KvCut));
 }
 
 MLA_API mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uint32_t* input_row_offsets,

@@ -47,8 +47,24 @@ struct KvAttentionArgs {
 
 enum KvKind { KV_F32, KV_BF16, KV_E4M3 };
 
+// Partial results of the split attention: every workgroup leaves at most two (the item its share begins
+// in and the one it ends in), of 32 rows of output sums, references and sums per row group.
+constexpr int kKvGroups = 256;        // workgroups, one per CU
+struct KvCut {                        // where a workgroup's share begins: tile 0 is the item's start
+    uint32_t b, kh, m, tile;
+    uint32_t t0, row0, rows, pad;     // the request's first token, the item's rows
+};
+// Groups of 32 rows (tokens x query heads of a key head) that an item of a call can have: up to 8.
+inline uint32_t kv_attention_row_groups(int64_t T, int64_t G)
+{
+    return (uint32_t)((T * G < 256 ? T * G : 256) + 31) / 32;
+}
+
 hipError_t launch_kv_write(const KvWriteArgs& a, bool fp8, bool half, hipStream_t s);
 hipError_t launch_kv_gather(const KvGatherArgs& a, KvKind kind, hipStream_t s);
+// Matrix-core form (heads of 64 and 128 columns), and whether it takes a call.
+bool kv_attention_mfma_fits(const KvAttentionArgs& a, KvKind kind);
+hipError_t launch_kv_attention_mfma(const KvAttentionArgs& a, KvKind kind, hipStream_t s);
 hipError_t launch_kv_attention(const KvAttentionArgs& a, KvKind kind, hipStream_t s);
 
 }  // namespace mla

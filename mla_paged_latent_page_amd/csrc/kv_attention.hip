@@ -253,6 +253,8 @@ hipError_t launch_kind(const KvAttentionArgs& a, hipStream_t s)
 
 hipError_t launch_kv_attention(const KvAttentionArgs& a, KvKind kind, hipStream_t s)
 {
+    if (kv_attention_mfma_fits(a, kind))
+        return launch_kv_attention_mfma(a, kind, s);
     return kind == KV_F32 ? launch_kind<KV_F32>(a, s) : kind == KV_BF16 ? launch_kind<KV_BF16>(a, s)
                                                                        : launch_kind<KV_E4M3>(a, s);
 }
