@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "kv.hpp"
 
@@ -30,8 +31,8 @@ constexpr int WAVES = 8;
 constexpr int TILE = 64;                     // positions of a step
 constexpr int WIDE = 256, NARROW = 128;      // rows of an item
 constexpr int STAGES = 4;
-constexpr int PAGE_SLOTS = 1024;             // page ids held in LDS
-constexpr uint32_t OVER = 128;               // an item counts as so many positions more than it has
+constexpr int PAGE_SLOTS = 128;              // page ids that a wave holds in LDS (pages of less than 8 positions)
+constexpr uint32_t OVER = 384;               // an item counts as so many positions more than it has
 constexpr uint32_t SNAP = 64;                // a cut so close to an end of an item is moved there
 constexpr uint32_t LEAST = 256;              // positions of the smallest share
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -39,6 +40,40 @@ constexpr float kSlack = 8.0f;               // the reference maximum may lag by
 constexpr float kNothing = -1e30f;           // the reference of a row that has seen nothing
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+// f(0), f(1), ..., f(N - 1) with constant arguments.
+template <class F, int... I>
+__device__ __attribute__((always_inline)) inline void each(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __attribute__((always_inline)) inline void each(F&& f)
+{
+    each(f, std::make_integer_sequence<int, N>{});
+}
+
+// The order of a step: NV products of weighted sums, then KB blocks of KS products of scores, and between
+// them the softmax of 16 KB elements.  The maximum is found beside the first TOP products; then the elements are
+// weighed, those of the first block beside the sums, the others beside the first block of scores; added
+// up one product later; and packed, in groups of 8, when their group's old weights have been used (DB
+// products each).
+template <int NV, int KS, int KB, int DB>
+struct Order {
+    static constexpr int TOP = NV >= 16 ? 4 : 2, E = 16 * KB, LAST = NV + KS - 2;
+    static constexpr int weighed(int i)      // elements weighed before product i
+    {
+        return i <= TOP ? 0 : i <= NV ? 16 * (i - TOP) / (NV - TOP) : i >= LAST ? E : 16 + (E - 16) * (i - NV) / (LAST - NV);
+    }
+    static constexpr int added(int i) { return i == 0 ? 0 : i == NV ? 16 : weighed(i - 1); }   // and added
+    static constexpr int packed(int g)       // the product that group g is packed behind
+    {
+        for (int i = 0; i < NV + KS * KB; ++i)
+            if (added(i + 1) >= 8 * (g + 1) && i >= DB * (g + 1) - 1)
+                return i;
+        return -1;
+    }
+};
 
 struct Params {
     KvAttentionArgs a;
@@ -262,36 +297,61 @@ __device__ inline f32x2 halves(float v)
     return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
+// lds_barrier() with the last operand reads (READS, of two instructions each) still in flight: what they read
+// is not written in the step that begins here.
+constexpr int READS = 4;                     // products that an operand is read ahead
+__device__ inline void step_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(%0)\n\ts_barrier" ::"n"(2 * READS) : "memory");
+}
+
+// This wave's LDS operations are done (step_barrier() counts on reads behind them).
+__device__ inline void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 template <int N>
 __device__ inline void wait_loads()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-// At most `tiles` (up to 3) tiles' worth of loads, N each, may be in flight.
+// The same for a number that is not constant, up to N.
 template <int N>
-__device__ inline void wait_tiles(uint32_t tiles)
+__device__ inline void wait_some(uint32_t left)
 {
-    if (tiles >= 3)
-        wait_loads<3 * N>();
-    else if (tiles == 2)
-        wait_loads<2 * N>();
-    else if (tiles == 1)
-        wait_loads<N>();
-    else
-        wait_loads<0>();
+    if constexpr (N > 0) {
+        if (left < N) {
+            wait_some<N - 1>(left);
+            return;
+        }
+    }
+    wait_loads<N>();
+}
+
+// The lane's number, worked out where it is needed.
+__device__ inline uint32_t lane_again()
+{
+    uint32_t x;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+    return x;
 }
 
 // 16 bytes per lane from a uniform base and a lane offset into LDS at lds + 16 * lane (see asm_ld16_lds).
 __device__ inline void load_lds16(const char* base, uint32_t voff, uint32_t lds)
 {
+    base = reinterpret_cast<const char*>(uniform(reinterpret_cast<uint64_t>(base)));
+    lds = uniform(lds);
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");
 }
+// 4 bytes per lane of the first sixteen (all lanes are on).
 __device__ inline void load_lds4(const void* src, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
+    lds = uniform(lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, 0xffff\n\tglobal_load_lds_dword %1, off\n\ts_mov_b64 exec, -1"
+                 :
+                 : "s"(lds), "v"(src)
+                 : "memory", "m0");
 }
 
 // Four e4m3 codes as bf16 (every code's value is one).
@@ -301,6 +361,20 @@ __device__ inline u32x2 bf16_of_codes(uint32_t x)
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true))};
 }
 
+// Whether a code is NaN (0x7F, 0xFF), and 0 in its place.
+__device__ inline bool nan4(uint32_t x) { return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+__device__ inline uint32_t zero_nan4(uint32_t x)
+{
+    const uint32_t bad = (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+    return x & ~(bad * 0xFFu);
+}
+
+// Whether one of two bf16 is not finite, and 0 in its place.
+__device__ inline uint32_t finite2(uint32_t x)
+{
+    x &= (x & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u;
+    return x & ((x & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : ~0u);
+}
 __device__ inline bool nonfinite2(uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; }
 
 // ---------------------------------------------------------------------------
@@ -311,26 +385,31 @@ __device__ inline bool nonfinite2(uint32_t x) { return (x & 0x7F80u) == 0x7F80u 
 // value rows by 64 bytes, fall on different banks (256 bytes are all of them).
 template <int D, bool FP8>
 struct Layout {
-    static constexpr int ROW = 2 * D, HALF = TILE * ROW, STAGE = 2 * HALF;
+    static constexpr int ROW = 2 * D, HALF = TILE * ROW;     // HALF: the keys, or the values, of a tile
     static constexpr int G = ROW / 16;                       // granules of a row
     __device__ static uint32_t fk(uint32_t x) { return D == 128 ? x & 15 : (x >> 1) & 7; }
     __device__ static uint32_t fv(uint32_t x) { return D == 128 ? 4 * (x & 3) : 4 * ((x >> 1) & 1); }
     // e4m3: codes as they are in memory, in a ring; two tiles of bf16, the one in use and the next.
     static constexpr int CODES_WAVE = 8 * 2 * D;             // a wave's eight rows of keys, then of values
     static constexpr int CODES = WAVES * CODES_WAVE;
-    // Scales: a wave's 8 + 8 floats (and as they come, repeated), for twice as many tiles, as they are
-    // read when the codes' place is filled again.
-    static constexpr int SCALES = WAVES * 256;
+    // Scales: a wave's 8 + 8 floats, for twice as many tiles, as they are read when the codes' place is
+    // filled again.
+    static constexpr int SCALES_WAVE = 64, SCALES = WAVES * SCALES_WAVE;
     static constexpr int SCALES_AT = STAGES * CODES;
-    static constexpr int TILES_AT = FP8 ? SCALES_AT + 2 * STAGES * SCALES : 0;
-    static constexpr int BUFFERS = FP8 ? 2 : STAGES;
-    static constexpr int PAGES_AT = TILES_AT + BUFFERS * STAGE;
-    static constexpr int FLAG_AT = PAGES_AT + PAGE_SLOTS * 4;
+    static constexpr int KEYS = FP8 ? 2 : 4, VALUES = FP8 ? 3 : 5;   // tiles of bf16 keys, and of values
+    static constexpr int ONES_AT = FP8 ? SCALES_AT + 2 * STAGES * SCALES : 0;
+    static constexpr int KEYS_AT = FP8 ? ONES_AT + SCALES : 0;
+    static constexpr int VALUES_AT = KEYS_AT + KEYS * HALF;
+    static constexpr int PAGES_AT = VALUES_AT + VALUES * HALF;
+    __device__ static uint32_t keys_at(int x) { return KEYS_AT + ((uint32_t)x & (KEYS - 1)) * HALF; }
+    __device__ static uint32_t values_at(int x) { return VALUES_AT + (uint32_t)(x + VALUES) % VALUES * HALF; }
+    static constexpr int FLAG_AT = PAGES_AT + WAVES * PAGE_SLOTS * 4;
     static constexpr int BYTES = FLAG_AT + 16;
     static constexpr int SUMS_WAVE = D / 32 * 16 * 256 + 512;   // a wave's output sums, references and sums
     static_assert(4 * SUMS_WAVE <= PAGES_AT && BYTES <= 163840, "LDS");
-    static constexpr int LOADS = FP8 ? (D == 128 ? 3 : 2) : (D == 128 ? 4 : 2);   // of a wave for a tile
-    static constexpr uint32_t AHEAD = FP8 ? 4 : 3;           // step t asks for tile t + AHEAD
+    // A wave's loads of a tile: its keys (and scales), its values.
+    static constexpr int KLOADS = FP8 ? (D == 128 ? 2 : 1) : (D == 128 ? 2 : 1), VLOADS = D == 128 && !FP8 ? 2 : 1;
+    static constexpr int LEAD = FP8 ? 6 : 4;                 // turn i asks for the keys of tile i + LEAD, the values of the one before
 };
 
 template <int D, bool FP8, bool PAGE8>
@@ -339,8 +418,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
     using Y = Layout<D, FP8>;
     constexpr int KS = D / 16, DB = D / 32;
     __shared__ __attribute__((aligned(1024))) char smem[Y::BYTES];
-    uint32_t* const ids = reinterpret_cast<uint32_t*>(smem + Y::PAGES_AT);
-    uint32_t* const flag = reinterpret_cast<uint32_t*>(smem + Y::FLAG_AT);
+    uint32_t* const flags = reinterpret_cast<uint32_t*>(smem + Y::FLAG_AT);   // of the last four tiles
     const KvAttentionArgs& a = P.a;
     const int lane = threadIdx.x & 63;
     const uint32_t wave = uniform(threadIdx.x >> 6);
@@ -385,29 +463,25 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
     }
     if (idle)
         return;
-    if (threadIdx.x == 0)
-        *flag = 0xFFFFFFFFu;
+    if (threadIdx.x < 4)
+        flags[threadIdx.x] = 0xFFFFFFFFu;
+    if (FP8 && threadIdx.x < Y::SCALES / 4)
+        reinterpret_cast<float*>(smem + Y::ONES_AT)[threadIdx.x] = 1.0f;
     uint32_t sequence = 0;                   // tiles this workgroup has had
 
     const uint32_t lds0 = lds_addr(smem);
-    // Lane-constant offsets of the operand reads.
-    uint32_t k_off[KS], v_off[DB];
+    // Lane-constant offsets of the operand reads: of the first columns; those of others differ in single bits.
+    const uint32_t k0 = col * Y::ROW + ((half ^ Y::fk(col)) * 16);
+    uint32_t v0;
     {
-        const uint32_t k0 = col * Y::ROW + ((half ^ Y::fk(col)) * 16);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-            k_off[s] = k0 ^ (s * 32);
         // lane c of a 16-lane group addresses row c / 4 of four, and 8 bytes of 16 columns
         const uint32_t c16 = lane & 15, row = 4 * half + (c16 >> 2);
-        const uint32_t v0 = row * Y::ROW + (((2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ Y::fv(row)) * 16) + (c16 & 1) * 8;
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-            v_off[d] = Y::HALF + (v0 ^ (d * 64));
+        v0 = row * Y::ROW + (((2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1)) ^ Y::fv(row)) * 16) + (c16 & 1) * 8;
     }
     const float c = fabsf(a.scale) * kLog2e;   // a negative scale turns the queries' signs; 0 is not taken
     const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
     const float slack = kSlack / c;
-    const uint32_t st_token = (uint32_t)a.L.stride_token;   // PAGE8: 8 rows below 2^31 bytes
+    const uint32_t st_token = (uint32_t)a.L.stride_token;   // PAGE8: below 2^24
 
     auto process = [&](auto narrow, uint32_t tile0, uint32_t tile1) __attribute__((always_inline)) {
         constexpr bool N = decltype(narrow)::value;
@@ -415,8 +489,8 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
         const uint32_t group = N ? wave & 3 : wave, kb0 = N ? wave >> 2 : 0;
         const uint32_t row0 = it.m * (N ? NARROW : WIDE) + group * 32;
         const bool live = row0 < r.rows;
-        const uint32_t row = min(row0 + col, r.rows - 1), tok = row / P.G, g = row - tok * P.G;
-        const uint32_t pos = r.cached + tok;
+        const uint32_t my_row = min(row0 + col, r.rows - 1), my_tok = my_row / P.G;
+        const uint32_t pos = r.cached + my_tok;
         // positions seen: low .. low + count - 1, and those below sunk
         const uint32_t hi = min(pos + 1, a.capacity);
         const uint32_t low = a.window && pos + 1 > a.window ? min(pos + 1 - a.window, hi) : 0;
@@ -437,141 +511,331 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
 
         bf16x8 q[KS];
         {
-            const char* src = a.q + (int64_t)(r.t0 + tok) * a.q_st + (int64_t)(it.kh * P.G + g) * Y::ROW + half * 16;
+            const uint32_t head = it.kh * P.G + my_row - my_tok * P.G;
+            const char* src = a.q + (int64_t)(r.t0 + my_tok) * a.q_st + (int64_t)head * Y::ROW + half * 16;
 #pragma unroll
             for (int s = 0; s < KS; ++s)
                 q[s] = as_bf16x8(ld16(src + s * 32) ^ flip);
         }
 
-        const uint32_t n_tiles = tile1 - tile0;
-        auto tile_start = [&](uint32_t t) __attribute__((always_inline)) {
-            const uint32_t j = tile0 + t;
+        const uint32_t n = tile1 - tile0;
+        auto tile_start = [&](uint32_t x) __attribute__((always_inline)) {
+            const uint32_t j = tile0 + x;
             return (j < it.ns ? j : it.lo + (j - it.ns)) * TILE;
         };
-        // Page ids of tiles id0 .. id0 + hold - 1 of this item, P.ids each.
-        const uint32_t hold = PAGE_SLOTS / P.ids;
-        uint32_t id0 = 0;
         auto page_of = [&](uint32_t p) __attribute__((always_inline)) {
             return PAGE8 ? __umulhi(p, P.ps_magic) >> P.ps_shift : p / a.L.page_size;
         };
-        auto fetch_ids = [&](uint32_t t0) __attribute__((always_inline)) {
-            lds_barrier();
-            id0 = t0;
-            for (uint32_t k = threadIdx.x; k < hold * P.ids; k += 64 * WAVES) {
-                const uint32_t s = k / P.ids, e = k - s * P.ids;
-                if (t0 + s < n_tiles) {
-                    const uint32_t lp = min(page_of(tile_start(t0 + s)) + e, a.L.max_pages - 1);
-                    ids[k] = min(a.L.page_table[(size_t)it.b * a.L.max_pages + lp], a.L.num_pages - 1);
+        auto page_id = [&](uint32_t lp) __attribute__((always_inline)) {
+            const uint32_t id = a.L.page_table[(size_t)it.b * a.L.max_pages + min(lp, a.L.max_pages - 1)];
+            return min(id, a.L.num_pages - 1);
+        };
+        // This wave fetches rows 8 wave .. 8 wave + 7 of every tile; rows past the end repeat the last one.
+        // PAGE8: they are in one page, and lane x holds where, for tile id0 + x: the offset in the layer, with the
+        // last of the eight rows to read in its lowest bits (and the offset of the scales).  Else the wave's part of
+        // LDS holds P.ids page ids for each of `hold` tiles.
+        auto first_row = [&](uint32_t x) __attribute__((always_inline)) {
+            const uint32_t p = tile_start(x) + wave * 8;
+            return p < len ? p : (PAGE8 ? (len - 1) & ~7u : len - 1);
+        };
+        uint32_t* const my_ids = reinterpret_cast<uint32_t*>(smem + Y::PAGES_AT) + wave * PAGE_SLOTS;
+        const uint32_t hold = PAGE8 ? 64 : PAGE_SLOTS / P.ids;
+        uint32_t id0 = 0;
+        uint64_t at_reg = 0, scale_reg = 0;
+        auto fetch_ids = [&](uint32_t x0) __attribute__((always_inline)) {
+            id0 = x0;
+            if constexpr (PAGE8) {
+                const uint32_t p0 = first_row(min(x0 + lane, n - 1)), lp = page_of(p0);
+                const uint32_t id = page_id(lp), in_page = p0 - lp * a.L.page_size;
+                at_reg = (uint64_t)((int64_t)id * a.L.stride_page + (int64_t)in_page * a.L.stride_token) | min(len - 1 - p0, 7u);
+                if constexpr (FP8)
+                    scale_reg = (uint64_t)((int64_t)id * a.Ls.stride_page + (int64_t)in_page * a.Ls.stride_token);
+            } else {
+                for (uint32_t k = lane; k < hold * P.ids; k += 64) {
+                    const uint32_t s = k / P.ids, e = k - s * P.ids;
+                    my_ids[k] = page_id(page_of(first_row(min(x0 + s, n - 1))) + e);
                 }
             }
-            lds_barrier();
         };
-        fetch_ids(0);
 
         const int64_t head_bytes = (int64_t)it.kh * (FP8 ? D : 2 * D);
         const int64_t scale_bytes = (int64_t)(it.kh * D / 128) * 4;
-        // Loads of tile t: this wave fetches rows 8 wave .. 8 wave + 7 of keys and values; those past the
-        // end repeat the last one.
-        auto issue = [&](uint32_t t) __attribute__((always_inline)) {
-            const uint32_t start = tile_start(t), slot = t & (STAGES - 1);
-            const uint32_t* my_ids = ids + (t - id0) * P.ids;
-            if constexpr (PAGE8) {
-                // eight rows from a multiple of 8 on are in one page
-                uint32_t p0 = start + wave * 8;
-                p0 = p0 < len ? p0 : (len - 1) & ~7u;
-                const uint32_t lp = page_of(p0), in_page = p0 - lp * a.L.page_size, last = len - 1 - p0;
-                const uint32_t id = uniform(my_ids[lp - page_of(start)]);
-                const char* src = a.L.base + (int64_t)id * a.L.stride_page + (int64_t)in_page * a.L.stride_token + head_bytes;
-                if constexpr (!FP8 && D == 128) {
-                    const uint32_t dst = lds0 + slot * Y::STAGE + wave * 2048;
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        const uint32_t x = 4 * i + (lane >> 4);
-                        const uint32_t off = min(x, last) * st_token;
-                        load_lds16(src, off + (((lane & 15) ^ Y::fk(wave * 8 + x)) * 16), dst + i * 1024);
-                        load_lds16(src + a.L.stride_kv, off + (((lane & 15) ^ Y::fv(x)) * 16), dst + Y::HALF + i * 1024);
-                    }
-                } else if constexpr (!FP8) {
-                    const uint32_t dst = lds0 + slot * Y::STAGE + wave * 1024, x = lane >> 3;
-                    const uint32_t off = min(x, last) * st_token;
-                    load_lds16(src, off + (((lane & 7) ^ Y::fk(wave * 8 + x)) * 16), dst);
-                    load_lds16(src + a.L.stride_kv, off + (((lane & 7) ^ Y::fv(x)) * 16), dst + Y::HALF);
+        // Turn i asks for the keys of tile i + LEAD and for the values of the tile before.  What the keys'
+        // addresses were made of is kept for the values' turn.
+        constexpr int ROWSETS = !FP8 && D == 128 ? 2 : 1;
+        struct Source {
+            const char* src;                 // PAGE8: of the eight rows, uniform
+            uint32_t last;
+            const char* row[ROWSETS];        // else of the lane's rows
+        };
+        Source now{a.L.base, 0, {}}, one = now;   // of this turn's keys and its values
+        bool ask_keys = false, ask_vals = false;   // what the turn's loads are, and where they go
+        uint32_t k_dst = 0, v_dst = 0, s_dst = 0;
+        [[maybe_unused]] const char* scale_src = nullptr;
+        auto prepare = [&](int i, auto all) __attribute__((always_inline)) {
+            constexpr bool ALL = decltype(all)::value;   // there are keys and values to ask for, of known pages
+            const int kt = i + Y::LEAD, vt = kt - 1;
+            const bool keys = ALL || kt < (int)n, vals = ALL || (vt >= 0 && vt < (int)n);
+            [[maybe_unused]] constexpr uint32_t LR = Y::G;    // bf16: lanes of a row
+            one = now;
+            ask_keys = keys;
+            ask_vals = vals;
+            k_dst = uniform(lds0 + (FP8 ? (uint32_t)(i & (STAGES - 1)) * Y::CODES + wave * Y::CODES_WAVE
+                                                       : Y::keys_at(kt) + wave * 8 * Y::ROW));
+            v_dst = uniform(FP8 ? k_dst + Y::CODES_WAVE / 2 : lds0 + Y::values_at(vt) + wave * 8 * Y::ROW);
+            if (keys) {
+                if (!ALL && (uint32_t)kt >= id0 + hold)
+                    fetch_ids((uint32_t)kt);
+                [[maybe_unused]] const char* scale_at = nullptr;
+                if constexpr (PAGE8) {
+                    auto held = [&](uint64_t v) __attribute__((always_inline)) {
+                        const int x = (int)((uint32_t)kt - id0);
+                        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, x) |
+                               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), x) << 32;
+                    };
+                    const uint64_t at = held(at_reg);
+                    now.last = (uint32_t)at & 7;
+                    now.src = a.L.base + (int64_t)(at - now.last) + head_bytes;
+                    if constexpr (FP8)
+                        scale_at = a.Ls.base + (int64_t)held(scale_reg) +
+                                   (int64_t)min((uint32_t)lane & 7, now.last) * a.Ls.stride_token;
                 } else {
-                    const uint32_t dst = lds0 + slot * Y::CODES + wave * Y::CODES_WAVE;
-                    if constexpr (D == 128) {
-                        const uint32_t off = min((uint32_t)lane >> 3, last) * st_token + (lane & 7) * 16;
-                        load_lds16(src, off, dst);
-                        load_lds16(src + a.L.stride_kv, off, dst + 1024);
-                    } else {
-                        const uint32_t off = min(col >> 2, last) * st_token + (lane & 3) * 16;
-                        asm_gld16_lds(src + (half ? a.L.stride_kv : 0) + off, dst);
-                    }
-                    const char* sc = a.Ls.base + (int64_t)id * a.Ls.stride_page +
-                                     (int64_t)(in_page + min((uint32_t)lane & 7, last)) * a.Ls.stride_token + scale_bytes +
-                                     ((lane & 8) ? a.Ls.stride_kv : 0);
-                    load_lds4(sc, lds0 + Y::SCALES_AT + (t & (2 * STAGES - 1)) * Y::SCALES + wave * 256);
+                    const uint32_t* ids = my_ids + ((uint32_t)kt - id0) * P.ids;
+                    const uint32_t first = page_of(first_row((uint32_t)kt)), start = tile_start((uint32_t)kt) + wave * 8;
+                    auto at = [&](const PagedLayer& L, uint32_t x) __attribute__((always_inline)) {
+                        const uint32_t p = min(start + x, len - 1), lp = page_of(p);
+                        return L.base + (int64_t)ids[lp - first] * L.stride_page +
+                               (int64_t)(p - lp * L.page_size) * L.stride_token;
+                    };
+#pragma unroll
+                    for (uint32_t k = 0; k < ROWSETS; ++k)
+                        now.row[k] = at(a.L, FP8 ? (D == 128 ? lane >> 3 : col >> 2) : 64 / LR * k + lane / LR) + head_bytes;
+                    if constexpr (FP8)
+                        scale_at = at(a.Ls, lane & 7);
                 }
-            } else {
-                const uint32_t first = page_of(start);
-                auto at = [&](const PagedLayer& L, uint32_t x) __attribute__((always_inline)) {
-                    const uint32_t p = min(start + wave * 8 + x, len - 1), lp = page_of(p);
-                    return L.base + (int64_t)my_ids[lp - first] * L.stride_page +
-                           (int64_t)(p - lp * L.page_size) * L.stride_token;
-                };
-                if constexpr (!FP8) {
-                    constexpr uint32_t LR = D == 128 ? 16 : 8;   // lanes of a row
-#pragma unroll
-                    for (uint32_t i = 0; i < (D == 128 ? 2 : 1); ++i) {
-                        const uint32_t x = 64 / LR * i + lane / LR, dst = lds0 + slot * Y::STAGE + wave * 8 * Y::ROW + i * 1024;
-                        const char* src = at(a.L, x) + head_bytes;
-                        asm_gld16_lds(src + (((lane & (LR - 1)) ^ Y::fk(wave * 8 + x)) * 16), dst);
-                        asm_gld16_lds(src + a.L.stride_kv + (((lane & (LR - 1)) ^ Y::fv(x)) * 16), dst + Y::HALF);
-                    }
-                } else {
-                    const uint32_t dst = lds0 + slot * Y::CODES + wave * Y::CODES_WAVE;
-                    if constexpr (D == 128) {
-                        const char* src = at(a.L, lane >> 3) + head_bytes + (lane & 7) * 16;
-                        asm_gld16_lds(src, dst);
-                        asm_gld16_lds(src + a.L.stride_kv, dst + 1024);
-                    } else {
-                        asm_gld16_lds(at(a.L, col >> 2) + head_bytes + (half ? a.L.stride_kv : 0) + (lane & 3) * 16, dst);
-                    }
-                    load_lds4(at(a.Ls, lane & 7) + scale_bytes + ((lane & 8) ? a.Ls.stride_kv : 0),
-                              lds0 + Y::SCALES_AT + (t & (2 * STAGES - 1)) * Y::SCALES + wave * 256);
+                if constexpr (FP8) {
+                    scale_src = scale_at + scale_bytes + ((lane & 8) ? a.Ls.stride_kv : 0);
+                    s_dst = uniform(lds0 + Y::SCALES_AT + (uint32_t)(kt & (2 * STAGES - 1)) * Y::SCALES +
+                                    wave * Y::SCALES_WAVE);
                 }
             }
         };
-        // e4m3: this wave's rows of tile t from codes to bf16.
-        auto convert = [&](uint32_t t) __attribute__((always_inline)) {
-            const char* src = smem + (t & (STAGES - 1)) * Y::CODES + wave * Y::CODES_WAVE + lane * 16;
-            char* dst = smem + Y::TILES_AT + (t & 1) * Y::STAGE;
+        // The turn's loads in PARTS parts: one after the other they would wait for one another (64 bytes per clock
+        // and CU), so that they are issued between products.
+        constexpr int PARTS = FP8 ? (D == 128 ? 3 : 2) : 2 * ROWSETS;
+        auto load_part = [&](int part) __attribute__((always_inline)) {
+            constexpr uint32_t LR = Y::G;    // bf16: lanes of a row
+            if constexpr (FP8) {
+                if (part == 0) {
+                    if (ask_keys)
+                        load_lds4(scale_src, s_dst);
+                    return;
+                }
+            }
+            if constexpr (FP8 && D == 64) {
+                // Half the lanes fetch keys, the others values (or keys again: not read).
+                if (ask_keys || ask_vals) {
+                    const bool v = half && ask_vals;
+                    const char* src;
+                    if constexpr (PAGE8)
+                        src = (v ? one.src : now.src) + __umul24(min(col >> 2, v ? one.last : now.last), st_token);
+                    else
+                        src = v ? one.row[0] : now.row[0];
+                    asm_gld16_lds(src + (v ? a.L.stride_kv : 0) + (lane & 3) * 16, uniform(k_dst));
+                }
+            } else {
+                auto load = [&](const Source& from, int64_t plus, uint32_t dst, uint32_t k, auto values) __attribute__((always_inline)) {
+                    const uint32_t x = FP8 ? lane >> 3 : 64 / LR * k + lane / LR;
+                    const uint32_t g = FP8 ? lane & 7
+                                           : (lane & (LR - 1)) ^ (decltype(values)::value ? Y::fv(x) : Y::fk(wave * 8 + x));
+                    if constexpr (PAGE8)
+                        load_lds16(from.src + plus, __umul24(min(x, from.last), st_token) + g * 16, dst + k * 1024);
+                    else
+                        asm_gld16_lds(from.row[k] + plus + g * 16, uniform(dst + k * 1024));
+                };
+                const int p = FP8 ? part - 1 : part;
+                if (p < ROWSETS) {
+                    if (ask_keys)
+                        load(now, 0, k_dst, p, std::false_type{});
+                } else if (ask_vals) {
+                    load(one, a.L.stride_kv, v_dst, p - ROWSETS, std::true_type{});
+                }
+            }
+        };
+        auto load_all = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+                load_part(k);
+        };
+        auto issue = [&](int i) __attribute__((always_inline)) {
+            prepare(i, std::false_type{});
+            load_all();
+        };
+        // Loads that a turn has asked for.
+        auto asked = [&](int i) __attribute__((always_inline)) {
+            const int kt = i + Y::LEAD, vt = kt - 1;
+            if (FP8 && D == 64)              // the scales; keys and values together
+                return (kt < (int)n ? 1u : 0u) + (kt < (int)n || (vt >= 0 && vt < (int)n) ? 1u : 0u);
+            return (kt < (int)n ? (uint32_t)Y::KLOADS : 0u) + (vt >= 0 && vt < (int)n ? (uint32_t)Y::VLOADS : 0u);
+        };
+        // Waits until turn i - M is done, turns up to i - 1 having been issued.
+        auto wait_turns = [&](int i, auto turns) __attribute__((always_inline)) {
+            constexpr int M = decltype(turns)::value, ALL = (M - 1) * (Y::KLOADS + Y::VLOADS);
+            if (i - 1 + Y::LEAD < (int)n && i - M + 1 + Y::LEAD >= 1) {
+                wait_loads<ALL>();
+                return;
+            }
+            uint32_t left = 0;
+#pragma unroll
+            for (int k = 1; k < M; ++k)
+                left += asked(i - k);
+            wait_some<ALL>(left);
+        };
+        // Whether some row of the item does not see all of a tile.  Such rows of values may hold anything, and a
+        // weight of 0 would turn infinities and NaN into NaN: each wave looks at its eight rows, puts zeros in
+        // their place and raises the tile's flag.  The rows that do see them get them behind the product.
+        auto ragged = [&](uint32_t start) __attribute__((always_inline)) {
+            return start + TILE > b_hi0 || (start < b_low1 && start + TILE > b_sunk0);
+        };
+        auto raise = [&](uint32_t x) __attribute__((always_inline)) {
+            if (lane == 0)
+                flags[x & 3] = sequence + x;
+        };
+        // bf16: the loads that step x needs (keys of tile x + 1, values of tile x) are done.
+        auto ready = [&](int x) __attribute__((always_inline)) {
+            if constexpr (!FP8) {
+                wait_turns(x, std::integral_constant<int, 3>{});
+                if (x >= 0 && x < (int)n && ragged(tile_start((uint32_t)x))) {
+                    char* mine = smem + Y::values_at(x) + wave * 8 * Y::ROW + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < 8 * Y::ROW / 1024; ++i) {
+                        u32x4 v = lds_ld16(mine + i * 1024);
+                        if (__any(nonfinite2(v[0]) || nonfinite2(v[1]) || nonfinite2(v[2]) || nonfinite2(v[3]))) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                v[k] = finite2(v[k]);
+                            lds_st16(mine + i * 1024, v);
+                            raise((uint32_t)x);
+                        }
+                    }
+                    wait_lds();
+                }
+            }
+        };
+        // e4m3: this wave's rows from codes to bf16, as turn i - 4 loaded them: keys of tile i + 2, values of tile
+        // i + 1.  In three parts, to go between products.
+        [[maybe_unused]] u32x4 codes[2] = {};
+        auto convert = [&](int i, bool all, int part) __attribute__((always_inline)) {
+            const bool keys = all || i + 2 < (int)n, vals = all || (i + 1 >= 0 && i + 1 < (int)n);
             auto put = [&](u32x4 x, char* to, uint32_t rr, uint32_t gr, uint32_t f) __attribute__((always_inline)) {
                 const u32x2 c0 = bf16_of_codes(x[0]), c1 = bf16_of_codes(x[1]), c2 = bf16_of_codes(x[2]), c3 = bf16_of_codes(x[3]);
                 lds_st16(to + rr * Y::ROW + ((gr ^ f) * 16), u32x4{c0[0], c0[1], c1[0], c1[1]});
                 lds_st16(to + rr * Y::ROW + (((gr + 1) ^ f) * 16), u32x4{c2[0], c2[1], c3[0], c3[1]});
             };
+            if (part == 0) {
+                if (all)
+                    wait_loads<3 * (Y::KLOADS + Y::VLOADS)>();
+                else
+                    wait_turns(i, std::integral_constant<int, 4>{});
+                const char* src = smem + (i & (STAGES - 1)) * Y::CODES + wave * Y::CODES_WAVE + lane * 16;
+                codes[0] = lds_ld16(src);
+                if constexpr (D == 128)
+                    codes[1] = lds_ld16(src + 1024);
+                return;
+            }
+            if (part == 1) {
+                // Values, and scales of values, that are not finite in a tile that some row does not see whole.
+                if (all || !vals || !ragged(tile_start((uint32_t)i + 1)))
+                    return;
+                u32x4& x = codes[D == 128 ? 1 : 0];
+                const bool values = D == 128 || half;
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    bad |= values && nan4(x[k]);
+                float* sv = reinterpret_cast<float*>(smem + Y::SCALES_AT + ((i + 1) & (2 * STAGES - 1)) * Y::SCALES +
+                                                     wave * Y::SCALES_WAVE) + 8 + (lane & 7);
+                const bool bad_scale = !(fabsf(*sv) < INFINITY);
+                if (__any(bad || bad_scale)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k] = values ? zero_nan4(x[k]) : x[k];
+                    if (bad_scale)
+                        *sv = 0.0f;
+                    raise((uint32_t)i + 1);
+                }
+                return;
+            }
+            char* k_to = smem + Y::keys_at(i);
+            char* v_to = smem + Y::values_at(i + 1);
             if constexpr (D == 128) {
-                const u32x4 k = lds_ld16(src), v = lds_ld16(src + 1024);
                 const uint32_t rr = wave * 8 + (lane >> 3), gr = 2 * (lane & 7);
-                put(k, dst, rr, gr, Y::fk(rr));
-                put(v, dst + Y::HALF, rr, gr, Y::fv(rr));
+                if (part == 2 && keys)
+                    put(codes[0], k_to, rr, gr, Y::fk(rr));
+                if (part == 3 && vals)
+                    put(codes[1], v_to, rr, gr, Y::fv(rr));
             } else {
-                const u32x4 x = lds_ld16(src);
                 const uint32_t rr = wave * 8 + (col >> 2), gr = 2 * (lane & 3);
-                put(x, dst + (half ? Y::HALF : 0), rr, gr, half ? Y::fv(rr) : Y::fk(rr));
+                if (part == 2 && (half ? vals : keys))
+                    put(codes[0], half ? v_to : k_to, rr, gr, half ? Y::fv(rr) : Y::fk(rr));
             }
         };
-        // e4m3: scales (keys 0, values 1) of rows 8 i + 4 half .. + 3 of tile t.
-        auto scales_of = [&](uint32_t t, uint32_t side, uint32_t i) __attribute__((always_inline)) {
-            return *reinterpret_cast<const f32x4*>(smem + Y::SCALES_AT + (t & (2 * STAGES - 1)) * Y::SCALES + i * 256 +
-                                                   side * 32 + half * 16);
+        auto convert_all = [&](int i) __attribute__((always_inline)) {
+            if constexpr (FP8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    convert(i, false, k);
+        };
+        // Steps plain0 .. plain1 - 1 are plain ones: all rows see all of the tiles t - 1 to t + 1, behind the first
+        // positions, and the turn's tiles are whole and their pages' ids at hand.
+        uint32_t plain0 = 0, plain1 = 0;
+        auto find_plain = [&](uint32_t t) __attribute__((always_inline)) {
+            // tiles x0 .. x1 - 1 are not ragged, and behind the first positions (or there are none)
+            const uint32_t sunk_tiles = it.ns > tile0 ? it.ns - tile0 : 0;
+            const uint32_t low_tile = (b_low1 + TILE - 1) / TILE, x_low = it.ns + (low_tile > it.lo ? low_tile - it.lo : 0);
+            const uint32_t x0 = max(sunk_tiles, x_low > tile0 ? x_low - tile0 : 0);
+            const uint32_t hi_tile = it.ns + (b_hi0 / TILE > it.lo ? b_hi0 / TILE - it.lo : 0);
+            const uint32_t x1 = hi_tile > tile0 ? min(hi_tile - tile0, n) : 0;
+            const uint32_t whole_tile = it.ns + (len / TILE > it.lo ? len / TILE - it.lo : 0);
+            const uint32_t whole = whole_tile > tile0 ? min(whole_tile - tile0, n) : 0;
+            const uint32_t most = min(whole, id0 + hold), ahead = Y::LEAD + 1;
+            plain0 = max(max(x0 + 1, sunk_tiles + 1), t);
+            plain1 = min(x1 > 0 ? x1 - 1 : 0, most > ahead ? most - ahead : 0);
+        };
+        auto prepare_turn = [&](int i, bool plain) __attribute__((always_inline)) {
+            if (plain) {
+                prepare(i, std::true_type{});
+            } else {
+                const uint32_t had = id0;
+                prepare(i, std::false_type{});
+                if (id0 != had)
+                    find_plain((uint32_t)i);
+            }
+        };
+        // Turn i, behind the barrier of step i.
+        auto turn = [&](int i) __attribute__((always_inline)) {
+            convert_all(i);
+            prepare_turn(i, false);
+            load_all();
+        };
+        // e4m3: scales (keys 0, values 1) of rows 8 i + 4 half .. + 3 of tile x.
+        auto scales_at = [&](uint32_t x) __attribute__((always_inline)) {
+            return Y::SCALES_AT + (x & (2 * STAGES - 1)) * Y::SCALES;
+        };
+        auto scales_of = [&](uint32_t at, uint32_t side, uint32_t i) __attribute__((always_inline)) {
+            return *reinterpret_cast<const f32x4*>(smem + at + i * Y::SCALES_WAVE + side * 32 + half * 16);
         };
 
-        for (uint32_t t = 0; t < Y::AHEAD && t < n_tiles; ++t)
-            issue(t);
+        lds_barrier();                       // the LDS of the item before is no longer read
+        fetch_ids(0);
+        find_plain(1);
         if constexpr (FP8) {
-            wait_tiles<Y::LOADS>(min(n_tiles - 1, 3u));
-            convert(0);
+            for (int i = -Y::LEAD; i < -2; ++i)
+                issue(i);
+            turn(-2);
+        } else {
+            for (int i = -Y::LEAD; i < -1; ++i)
+                issue(i);
         }
 
         f32x16 o[DB];
@@ -581,204 +845,329 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
             for (int e = 0; e < 16; ++e)
                 o[d][e] = 0.0f;
         float mref = kNothing, l = 0.0f;
-
-        for (uint32_t t = 0; t < n_tiles; ++t) {
-            // Tile t is there (e4m3: this wave's codes of tile t + 1 are), for every wave, and the one before
-            // is no longer read.
-            if constexpr (FP8)
-                wait_tiles<Y::LOADS>(n_tiles - 1 > t + 1 ? min(n_tiles - 2 - t, 2u) : 0u);
-            else
-                wait_tiles<Y::LOADS>(min(n_tiles - 1 - t, 2u));
-            lds_barrier();
-            const uint32_t ask = t + Y::AHEAD;
-            if (ask < n_tiles) {
-                if (ask >= id0 + hold)
-                    fetch_ids(ask);
-                issue(ask);
-            }
-            const uint32_t start = tile_start(t);
-            const char* tl = smem + Y::TILES_AT + (t & (Y::BUFFERS - 1)) * Y::STAGE;
-            if constexpr (FP8)
-                if (t + 1 < n_tiles)
-                    convert(t + 1);
-
-            // Rows that some do not see may hold anything: a weight of 0 would turn their infinities and
-            // NaN into NaN.  Where a tile has such rows, every wave looks at its eight of them.
-            bool dirty = false;
-            ++sequence;
-            if (start + TILE > b_hi0 || (start < b_low1 && start + TILE > b_sunk0)) {
-                bool bad = false;
+        f32x16 s[KB];                        // scores of tile t, then its weights
+        bf16x8 w8[KB][2];                    // weights of tile t - 1, then of tile t, as operands
 #pragma unroll
-                for (int i = 0; i < 8 * Y::ROW / 1024; ++i) {
-                    const u32x4 x = lds_ld16(tl + Y::HALF + wave * 8 * Y::ROW + i * 1024 + lane * 16);
-                    bad |= nonfinite2(x[0]) || nonfinite2(x[1]) || nonfinite2(x[2]) || nonfinite2(x[3]);
-                }
-                if (__any(bad) && lane == 0)
-                    *flag = sequence;
-                lds_barrier();
-                dirty = uniform(*flag) == sequence;
-            }
-            // No row of this wave sees any of it?
-            const uint32_t my0 = start + kb0 * 32, my1 = my0 + KB * 32;
-            if (!live || my0 >= w_hi1 || (my1 <= w_low0 && my0 >= min(a.sinks, w_low1)))
-                continue;
+        for (int b = 0; b < KB; ++b)
+            w8[b][0] = w8[b][1] = as_bf16x8(u32x4{0u, 0u, 0u, 0u});
 
-            f32x16 s[KB];
+        // Does some row of this wave see some of tile x?
+        auto sees_some = [&](uint32_t x) __attribute__((always_inline)) {
+            const uint32_t my0 = tile_start(x) + kb0 * 32, my1 = my0 + KB * 32;
+            return live && my0 < w_hi1 && !(my1 <= w_low0 && my0 >= min(a.sinks, w_low1));
+        };
+        // Scores of the first tile.  Operands are read READS products ahead, which the fences keep the compiler to.
+        auto scores = [&](uint32_t x) __attribute__((always_inline)) {
+            const uint32_t kt = Y::keys_at((int)x) + kb0 * 32 * Y::ROW + k0;
+            constexpr int NP = KS * KB;
+            bf16x8 k8[READS];
+            auto operand = [&](int i) __attribute__((always_inline)) {
+                return as_bf16x8(lds_ld16(smem + (kt ^ (i / KB * 32)) + i % KB * 32 * Y::ROW));
+            };
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
+            for (int i = 0; i < READS && i < NP; ++i)
+                k8[i] = operand(i);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     s[b][e] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        as_bf16x8(lds_ld16(tl + k_off[k] + (kb0 + b) * 32 * Y::ROW)), q[k], s[b], 0, 0, 0);
+            for (int i = 0; i < NP; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                s[i % KB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8[i % READS], q[i / KB], s[i % KB], 0, 0, 0);
+                if (i + READS < NP)
+                    k8[i % READS] = operand(i + READS);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // Element 4 i + e of block b of a tile's scores is position 32 (kb0 + b) + 8 i + 4 half + e of it.
+        // e4m3: the scales of the keys.
+        auto scale_keys = [&](uint32_t x) __attribute__((always_inline)) {
             if constexpr (FP8) {
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const f32x4 f = scales_of(t, 0, (kb0 + b) * 4 + i);
+                        const f32x4 f = scales_of(scales_at(x), 0, (kb0 + b) * 4 + i);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             s[b][4 * i + e] *= f[e];
                     }
             }
-            // element 4 i + e of block b is position my0 + 32 b + 8 i + 4 half + e
-            auto seen = [&](int b, int e) __attribute__((always_inline)) {
-                const uint32_t p = my0 + 32 * b + 8 * (e / 4) + 4 * half + e % 4;
-                return p - low < count || p < sunk;
+        };
+        // What rows do not see.
+        auto mask = [&](uint32_t x, bool visible) __attribute__((always_inline)) {
+            const uint32_t my0 = tile_start(x) + kb0 * 32, my1 = my0 + KB * 32;
+            if (!visible || my1 > w_hi0 || (my0 < w_low1 && my1 > w_sunk0)) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t p = my0 + 32 * b + 8 * (e / 4) + 4 * half + e % 4;
+                        s[b][e] = visible && (p - low < count || p < sunk) ? s[b][e] : -INFINITY;
+                    }
+            }
+        };
+        bf16x8 x8[READS];                    // operands of the next products
+        auto read_first = [&](int x) __attribute__((always_inline)) {
+            const uint32_t vt = Y::values_at(x) + kb0 * 32 * Y::ROW + v0;
+#pragma unroll
+            for (int i = 0; i < READS; ++i) {
+                const char* at = smem + (vt ^ (i % DB * 64)) + i / DB * 16 * Y::ROW;
+                x8[i] = join8(lds_tr16(at), lds_tr16(at + 8 * Y::ROW));
+            }
+        };
+        // The weighted sums of the last tile.
+        auto last_sums = [&]() __attribute__((always_inline)) {
+            const uint32_t vt = Y::values_at((int)n - 1) + kb0 * 32 * Y::ROW + v0;
+            constexpr int NP = DB * 2 * KB;
+            auto operand = [&](int i) __attribute__((always_inline)) {
+                const char* at = smem + (vt ^ (i % DB * 64)) + i / DB * 16 * Y::ROW;
+                return join8(lds_tr16(at), lds_tr16(at + 8 * Y::ROW));
             };
-            const bool masked = my1 > w_hi0 || (my0 < w_low1 && my1 > w_sunk0);
-            if (masked) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x8[i % READS], w8[i / (2 * DB)][i / DB % 2], o[i % DB], 0, 0, 0);
+                if (i + READS < NP)
+                    x8[i % READS] = operand(i + READS);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // What was not finite in the values of tile x, from the pool, one position at a time, for the rows that
+        // see it.  (Its weights are still the operands'.)
+        auto add_nonfinite = [&](uint32_t x) __attribute__((always_inline)) {
+            const uint32_t my0 = tile_start(x) + kb0 * 32;
+#pragma unroll 1
+            for (uint32_t k = 0; k < 32u * KB; ++k) {
+                const uint32_t p = my0 + k;
+                if (p >= len)
+                    break;
+                const bool sees = p - low < count || p < sunk;
+                // position k is element 16 (k / 32) + (k % 32) / 8 * 4 + k % 4 of half (k / 4) % 2
+                const uint32_t e0 = (k >> 5) * 16 + ((k >> 3) & 3) * 4 + (k & 3);
+                uint32_t pair = 0;
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        s[b][e] = seen(b, e) ? s[b][e] : -INFINITY;
-            }
-            float top;
-            {
-                float x[4] = {s[0][0], s[0][1], s[0][2], s[0][3]};
+                    for (int e = 0; e < 8; ++e)
+                        pair = e0 / 2 == (uint32_t)(8 * b + e) ? __builtin_bit_cast(u32x4, w8[b][e / 4])[e % 4] : pair;
+                const f32x2 h = halves(e0 & 1 ? bf16_hi(pair) : bf16_lo(pair));
+                const float w = (k >> 2) & 1 ? h[1] : h[0];
+                const char* v = a.L.base + token_offset(a.L, it.b, p) + a.L.stride_kv + head_bytes + half * (FP8 ? 4 : 8);
+                bool whole = false;          // e4m3: a scale that is not finite makes all columns NaN
+                if constexpr (FP8)
+                    whole = !(fabsf(*reinterpret_cast<const float*>(a.Ls.base + token_offset(a.Ls, it.b, p) + a.Ls.stride_kv +
+                                                                    scale_bytes)) < INFINITY);
 #pragma unroll
-                for (int b = 0; b < KB; ++b)
+                for (int d = 0; d < DB; ++d)
 #pragma unroll
-                    for (int e = b ? 0 : 4; e < 16; ++e)
-                        x[e & 3] = __builtin_elementwise_maximum(x[e & 3], s[b][e]);
-                const f32x2 h = halves(__builtin_elementwise_maximum(__builtin_elementwise_maximum(x[0], x[1]),
-                                                                     __builtin_elementwise_maximum(x[2], x[3])));
-                top = __builtin_elementwise_maximum(h[0], h[1]);
+                    for (int i = 0; i < 4; ++i) {
+                        // columns 32 d + 8 i + 4 half .. + 3
+                        u32x2 y;
+                        if constexpr (FP8)
+                            y = bf16_of_codes(*reinterpret_cast<const uint32_t*>(v + 32 * d + 8 * i));
+                        else
+                            y = *reinterpret_cast<const u32x2*>(v + 64 * d + 16 * i);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float z = whole ? NAN : e & 1 ? bf16_hi(y[e / 2]) : bf16_lo(y[e / 2]);
+                            if (sees && !(fabsf(z) < INFINITY))
+                                o[d][4 * i + e] += w * z;
+                        }
+                    }
             }
-            if (__any(top > mref + slack)) {
-                const float now = fmaxf(mref, top);
-                const float f = __builtin_amdgcn_exp2f((mref - now) * c);
-                mref = now;
+        };
+
+        // The products of a step, of 32 cycles each, with the softmax between
+        // them, five or six other instructions to a product.  The scores' first block is free, and taken by the next
+        // tile's, once its weights are operands.
+        auto whole_step = [&](uint32_t t, bool plain) __attribute__((always_inline)) {
+            const uint32_t vt = Y::values_at((int)t - 1) + kb0 * 32 * Y::ROW + v0;
+            const uint32_t vn = Y::values_at((int)t) + kb0 * 32 * Y::ROW + v0;
+            const uint32_t kt = Y::keys_at((int)t + 1) + kb0 * 32 * Y::ROW + k0;
+            constexpr int NV = DB * 2 * KB, NP = NV + KS * KB;
+            [[maybe_unused]] const uint32_t ks_at = plain ? scales_at(t) : (uint32_t)Y::ONES_AT, vs_at = scales_at(t);
+            auto operand = [&](int i) __attribute__((always_inline)) {
+                if (i < NV || i >= NP) {     // (behind the last: the next step's first)
+                    const int k = i < NV ? i : i - NP;
+                    const char* at = smem + ((i < NV ? vt : vn) ^ (k % DB * 64)) + k / DB * 16 * Y::ROW;
+                    return join8(lds_tr16(at), lds_tr16(at + 8 * Y::ROW));
+                }
+                const int j = i - NV;        // block by block
+                return as_bf16x8(lds_ld16(smem + (kt ^ (j % KS * 32)) + j / KS * 32 * Y::ROW));
+            };
+            float y[4], base = 0.0f, f = 1.0f, part[4] = {};
+            bool some = false;
+            f32x4 vs = {};
+            auto scale = [&](int e0, int e1) __attribute__((always_inline)) {
+                if constexpr (FP8)
+#pragma unroll
+                    for (int e = e0; e < e1; e += 4) {
+                        const f32x4 z = scales_of(ks_at, 0, kb0 * 4 + e / 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            s[e / 16][e % 16 + k] *= z[k];
+                    }
+            };
+            auto greatest = [&](int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = e0; e < e1; ++e)
+                    y[e & 3] = e < 4 ? s[0][e] : __builtin_elementwise_maximum(y[e & 3], s[e / 16][e % 16]);
+            };
+            auto reference = [&]() __attribute__((always_inline)) {
+                const f32x2 h = halves(__builtin_elementwise_maximum(__builtin_elementwise_maximum(y[0], y[1]),
+                                                                     __builtin_elementwise_maximum(y[2], y[3])));
+                const float top = __builtin_elementwise_maximum(h[0], h[1]);
+                const bool more = top > mref + slack;
+                some = __any(more);
+                const float next = more ? top : mref;
+                f = __builtin_amdgcn_exp2f((mref - next) * c);
+                mref = next;
                 l *= f;
+                base = -next * c;
+            };
+            auto weigh = [&](int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = e0; e < e1; ++e)
+                    s[e / 16][e % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 16][e % 16], c, base));
+            };
+            auto add = [&](int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+                for (int e = e0; e < e1; ++e) {
+                    part[e & 3] += s[e / 16][e % 16];
+                    if constexpr (FP8) {
+                        if (e % 4 == 0 || e == e0)
+                            vs = scales_of(vs_at, 1, kb0 * 4 + e / 4);
+                        s[e / 16][e % 16] *= vs[e % 4];
+                    }
+                }
+                if (e1 > e0)
+                    asm volatile("" : "+v"(part[0]), "+v"(part[1]), "+v"(part[2]), "+v"(part[3]));
+            };
+            auto pack = [&](int g) __attribute__((always_inline)) {
+                const f32x16& z = s[g / 2];
+                const int k = g % 2 * 8;
+                u32x4 x = {pack_bf16x2(z[k], z[k + 1]), pack_bf16x2(z[k + 2], z[k + 3]), pack_bf16x2(z[k + 4], z[k + 5]),
+                           pack_bf16x2(z[k + 6], z[k + 7])};
+                asm volatile("" : "+v"(x));   // (here: the compiler would move it all behind the branch below)
+                w8[g / 2][g % 2] = as_bf16x8(x);
+            };
+            using Z = Order<NV, KS, KB, DB>;
+            each<NP>([&](auto step) __attribute__((always_inline)) {
+                constexpr int i = decltype(step)::value;
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (i < NV) {
+                    o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x8[i % READS], w8[i / (2 * DB)][i / DB % 2], o[i % DB], 0,
+                                                                        0, 0);
+                } else {
+                    constexpr int j = i - NV, b = j / KS;
+                    if constexpr (j % KS == 0)
+                        s[b] = f32x16{};     // (its weights are operands)
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x8[i % READS], q[j % KS], s[b], 0, 0, 0);
+                }
+                x8[(i + READS) % NP % READS] = operand(i + READS);
+                if constexpr (i < Z::TOP - 1) {
+                    scale(Z::E * i / (Z::TOP - 1) / 4 * 4, Z::E * (i + 1) / (Z::TOP - 1) / 4 * 4);
+                    greatest(Z::E * i / (Z::TOP - 1) / 4 * 4, Z::E * (i + 1) / (Z::TOP - 1) / 4 * 4);
+                }
+                if constexpr (i == Z::TOP - 1)
+                    reference();
+                weigh(Z::weighed(i), Z::weighed(i + 1));
+                add(Z::added(i), Z::added(i + 1));
+                each<2 * KB>([&](auto g) __attribute__((always_inline)) {
+                    if constexpr (Z::packed(decltype(g)::value) == i)
+                        pack(g);
+                });
+                // the turn: e4m3's conversion and the loads, one by one
+                if constexpr (FP8) {
+                    constexpr int AT[4] = {NP / 8, NP / 8 + 1, NP / 8 + 2, NP / 8 + 3};
+                    static_assert(AT[D == 128 ? 3 : 2] < NP - READS, "the writes are older than the last reads");
+                    each<4>([&](auto k) __attribute__((always_inline)) {
+                        if constexpr (AT[decltype(k)::value] == i)
+                            convert((int)t, plain, decltype(k)::value);
+                    });
+                }
+                constexpr int FROM = FP8 ? NP / 8 + 4 : 1, EVERY = (NP - FROM) / PARTS;
+                if constexpr (i == FROM - 1)
+                    prepare_turn((int)t, plain);
+                if constexpr (N) {           // (bound by memory: early)
+                    if constexpr (i == FROM)
+                        load_all();
+                } else if constexpr (i >= FROM && (i - FROM) % EVERY == 0 && (i - FROM) / EVERY < PARTS) {
+                    load_part((i - FROM) / EVERY);
+                }
+            });
+            __builtin_amdgcn_sched_barrier(0);
+            l += (part[0] + part[1]) + (part[2] + part[3]);
+            if (some) {
 #pragma unroll
                 for (int d = 0; d < DB; ++d)
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         o[d][e] *= f;
             }
-            const float base = mref * c;
-            float part[4] = {};
+        };
+
+        // Step t: the sums of tile t - 1, the softmax of tile t, the scores of tile t + 1.  (Before the first tile
+        // there are zeros; behind the last one, scores that nothing reads.)
+        {
+            char* mine = smem + Y::values_at(-1) + wave * 8 * Y::ROW + lane * 16;
 #pragma unroll
-            for (int b = 0; b < KB; ++b)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], c, -base));
-                    part[e & 3] += s[b][e];
-                }
-            l += (part[0] + part[1]) + (part[2] + part[3]);
-            if constexpr (FP8) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 f = scales_of(t, 1, (kb0 + b) * 4 + i);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            s[b][4 * i + e] *= f[e];
-                    }
-                if (masked) {   // (0 times an infinite scale)
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            s[b][e] = seen(b, e) ? s[b][e] : 0.0f;
-                }
-            }
-            auto weights = [&](int b, int st) __attribute__((always_inline)) {
-                const f32x16& x = s[b];
-                return as_bf16x8(u32x4{pack_bf16x2(x[8 * st], x[8 * st + 1]), pack_bf16x2(x[8 * st + 2], x[8 * st + 3]),
-                                       pack_bf16x2(x[8 * st + 4], x[8 * st + 5]), pack_bf16x2(x[8 * st + 6], x[8 * st + 7])});
-            };
-            auto values = [&](int b, int st, int d) __attribute__((always_inline)) {
-                const char* at = tl + v_off[d] + ((kb0 + b) * 32 + st * 16) * Y::ROW;
-                return join8(lds_tr16(at), lds_tr16(at + 8 * Y::ROW));
-            };
-            if (!dirty) {
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        const bf16x8 p = weights(b, st);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values(b, st, d), p, o[d], 0, 0, 0);
-                    }
-            } else {
-                // With what is not finite left out; then that, one position at a time, for the rows that see it.
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        const bf16x8 p = weights(b, st);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            u32x4 v = __builtin_bit_cast(u32x4, values(b, st, d));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                v[k] &= (v[k] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : ~0u;
-                                v[k] &= (v[k] & 0x7F800000u) == 0x7F800000u ? 0x0000FFFFu : ~0u;
-                            }
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(v), p, o[d], 0, 0, 0);
-                        }
-                    }
-#pragma unroll 1
-                for (uint32_t k = 0; k < 32u * KB; ++k) {
-                    const uint32_t p = my0 + k;
-                    const bool sees = p - low < count || p < sunk;
-                    // position k is element 16 (k / 32) + (k % 32) / 8 * 4 + k % 4 of half (k / 4) % 2
-                    const uint32_t e0 = (k >> 5) * 16 + ((k >> 3) & 3) * 4 + (k & 3);
-                    float x = 0.0f;
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            x = e0 == (uint32_t)(16 * b + e) ? s[b][e] : x;
-                    const f32x2 h = halves(x);
-                    x = (k >> 2) & 1 ? h[1] : h[0];
-                    const uint32_t vr = kb0 * 32 + k;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // columns 32 d + 8 i + 4 half .. + 3
-                            const uint32_t gr = 4 * d + i;
-                            const u32x2 v = *reinterpret_cast<const u32x2*>(tl + Y::HALF + vr * Y::ROW +
-                                                                            ((gr ^ Y::fv(vr)) * 16) + half * 8);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float y = e & 1 ? bf16_hi(v[e / 2]) : bf16_lo(v[e / 2]);
-                                if (sees && !(fabsf(y) < INFINITY))
-                                    o[d][4 * i + e] += x * y;
-                            }
-                        }
-                }
-            }
+            for (int i = 0; i < 8 * Y::ROW / 1024; ++i)
+                lds_st16(mine + i * 1024, u32x4{0u, 0u, 0u, 0u});
         }
+        ready(-1);
+        lds_barrier();
+        turn(-1);
+        bool weighed = false, visible = sees_some(0);   // tiles t - 1 and t
+        if (visible)
+            scores(0);
+#pragma unroll
+        for (int i = 0; i < READS; ++i)
+            x8[i] = as_bf16x8(u32x4{0u, 0u, 0u, 0u});
+        bool read = true;                    // x8 holds the first operands of the values of tile t - 1
+        for (uint32_t t = 0; t < n; ++t) {
+            const bool plain = t >= plain0 && t < plain1;
+            if (plain && !FP8)
+                wait_loads<2 * (Y::KLOADS + Y::VLOADS)>();
+            else
+                ready((int)t);
+            step_barrier();
+            const bool next = plain ? live : t + 1 < n && sees_some(t + 1);
+            if (weighed || visible || next) {
+                if (!plain) {
+                    scale_keys(t);
+                    mask(t, visible);
+                    // the operands of tile t - 1 are gone behind this, so what it lacks is added first
+                    if (weighed && ragged(tile_start(t - 1)) && uniform(flags[(t - 1) & 3]) == sequence + t - 1)
+                        add_nonfinite(t - 1);
+                    if (!read)
+                        read_first((int)t - 1);
+                }
+                whole_step(t, plain);
+                read = true;
+            } else {
+                turn((int)t);
+                wait_lds();
+                read = false;
+            }
+            weighed = visible;
+            visible = next;
+        }
+        ready((int)n);
+        lds_barrier();
+        if (weighed) {
+            if (ragged(tile_start(n - 1)) && uniform(flags[(n - 1) & 3]) == sequence + n - 1)
+                add_nonfinite(n - 1);
+            last_sums();
+        }
+        sequence += n;
+
+        // (Worked out again: they would hold registers through all of the steps.)
+        const uint32_t ln = lane_again(), half = ln >> 5, col = ln & 31, lane = ln;
+        const uint32_t row = min(row0 + col, r.rows - 1), tok = row / P.G, g = row - tok * P.G;
 
         // The row's sum, over both halves; with two groups of waves, over both of them.
         {
@@ -787,7 +1176,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
         }
         bool mine = live;
         if constexpr (N) {
-            lds_barrier();                   // the tiles are no longer read
+            lds_barrier();                   // the tiles are no longer read by the others
             float* sums = reinterpret_cast<float*>(smem + group * Y::SUMS_WAVE);
             if (kb0 == 1 && live) {
 #pragma unroll
@@ -880,27 +1269,24 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
 // the join
 // ---------------------------------------------------------------------------
 // Block (cut w, 32 rows) with w the first cut inside an item: the sums that the shares around the item's
-// cuts left, each times its exp(reference - the largest one), in the order of the shares.  Four groups of
-// waves take every fourth piece.
-template <int D>
-__global__ void __launch_bounds__(1024) kv_attention_join(Params P)
+// cuts left, each times its exp(reference - the largest one), in the order of the shares.  SETS groups of four
+// waves take every SETS-th piece.
+template <int D, int SETS>
+__global__ void __launch_bounds__(256 * SETS) kv_attention_join(Params P)
 {
-    constexpr int DB = D / 32, Q = DB;       // a thread has Q quads of the row group's sums
-    const uint32_t w = blockIdx.x, group = blockIdx.y;
+    constexpr int Q = D / 32;                // a thread has Q quads of the row group's sums
+    const uint32_t w = blockIdx.x + 1, group = blockIdx.y;
     const uint32_t groups = P.cuts[kKvGroups].tile;
-    if (w == 0 || w >= groups)
+    const KvCut cut = P.cuts[w], prev = P.cuts[w - 1];
+    if (w >= groups || cut.tile == 0 || group * 32 >= cut.rows)
         return;
-    const KvCut cut = P.cuts[w];
-    if (cut.tile == 0 || group * 32 >= cut.rows)
-        return;
-    const KvCut prev = P.cuts[w - 1];
     auto same = [&](const KvCut& x) { return x.tile != 0 && x.b == cut.b && x.kh == cut.kh && x.m == cut.m; };
     if (same(prev))
         return;
     __shared__ uint32_t last;
     __shared__ bool empty[kKvGroups];        // shares that end where they begin leave nothing
-    __shared__ float top[4][64], all[4][64];
-    __shared__ f32x4 part[3][Q][256];
+    __shared__ float top[SETS][64], all[SETS][64];
+    __shared__ f32x4 part[SETS > 1 ? SETS - 1 : 1][Q][256];
     if (threadIdx.x == 0)
         last = groups - 1;
     __syncthreads();
@@ -920,49 +1306,62 @@ __global__ void __launch_bounds__(1024) kv_attention_join(Params P)
     auto piece = [&](uint32_t k) {
         return a.ws + (size_t)(k == 0 ? 2 * (w - 1) + 1 : 2 * (w + k - 1)) * P.piece + group * (32 * (D + 2));
     };
-    float mx = kNothing;
-    for (uint32_t k = set; k < pieces; k += 4)
-        if (k == 0 || !empty[k - 1])
-            mx = fmaxf(mx, piece(k)[32 * D + col]);
-    if (tid < 64)
-        top[set][lane] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(top[0][lane], top[1][lane]), fmaxf(top[2][lane], top[3][lane]));
-    float l = 0.0f;
+    float mx = kNothing, l = 0.0f;
     f32x4 sum[Q] = {};
     constexpr int U = 2;
-    for (uint32_t k0 = set; k0 < pieces; k0 += 4 * U) {
+    for (uint32_t k0 = set; k0 < pieces; k0 += SETS * U) {
         f32x4 v[U][Q];
         float m[U], s[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float* p = piece(min(k0 + 4 * u, pieces - 1));
+            const uint32_t k = k0 + SETS * u;
+            const float* p = piece(min(k, pieces - 1));
+            const bool on = k < pieces && (k == 0 || !empty[k - 1]);
             m[u] = p[32 * D + col];
             s[u] = p[32 * D + 32 + col];
 #pragma unroll
             for (int j = 0; j < Q; ++j)
                 v[u][j] = *reinterpret_cast<const f32x4*>(p + (j * 256 + tid) * 4);
+            m[u] = on ? m[u] : kNothing;
+            s[u] = on ? s[u] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < Q; ++j)
+                v[u][j] = on ? v[u][j] : f32x4{};
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (k0 + 4 * u < pieces && (k0 + 4 * u == 0 || !empty[k0 + 4 * u - 1])) {
-                const float f = __builtin_amdgcn_exp2f((m[u] - mx) * c);
-                l += s[u] * f;
+        for (int u = 0; u < U; ++u) {
+            const float now = fmaxf(mx, m[u]);
+            const float f0 = __builtin_amdgcn_exp2f((mx - now) * c), f1 = __builtin_amdgcn_exp2f((m[u] - now) * c);
+            mx = now;
+            l = l * f0 + s[u] * f1;
 #pragma unroll
-                for (int j = 0; j < Q; ++j)
-                    sum[j] += v[u][j] * f;
-            }
+            for (int j = 0; j < Q; ++j)
+                sum[j] = sum[j] * f0 + v[u][j] * f1;
+        }
     }
-    if (tid < 64)
-        all[set][lane] = l;
-    if (set > 0)
+    if constexpr (SETS > 1) {
+        if (tid < 64) {
+            top[set][lane] = mx;
+            all[set][lane] = l;
+        }
+        if (set > 0)
 #pragma unroll
-        for (int j = 0; j < Q; ++j)
-            part[set - 1][j][tid] = sum[j];
-    __syncthreads();
-    if (set > 0)
-        return;
-    l = (all[0][lane] + all[1][lane]) + (all[2][lane] + all[3][lane]);
+            for (int j = 0; j < Q; ++j)
+                part[set - 1][j][tid] = sum[j];
+        __syncthreads();
+        if (set > 0)
+            return;
+#pragma unroll
+        for (int k = 1; k < SETS; ++k) {
+            const float m1 = top[k][lane], now = fmaxf(mx, m1);
+            const float f0 = __builtin_amdgcn_exp2f((mx - now) * c), f1 = __builtin_amdgcn_exp2f((m1 - now) * c);
+            mx = now;
+            l = l * f0 + all[k][lane] * f1;
+#pragma unroll
+            for (int j = 0; j < Q; ++j)
+                sum[j] = sum[j] * f0 + part[k - 1][j][tid] * f1;
+        }
+    }
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     const uint32_t row = cut.row0 + group * 32 + col;
     if (group * 32 + col >= cut.rows)
@@ -973,7 +1372,7 @@ __global__ void __launch_bounds__(1024) kv_attention_join(Params P)
 #pragma unroll
     for (int j = 0; j < Q; ++j) {
         // quad j * 4 + tid / 64 of the lane: columns 32 j + 8 (tid / 64) + 4 (lane / 32) .. + 3
-        const f32x4 x = ((sum[j] + part[0][j][tid]) + (part[1][j][tid] + part[2][j][tid])) * inv;
+        const f32x4 x = sum[j] * inv;
         *reinterpret_cast<u32x2*>(out + 32 * j + 8 * (tid >> 6) + 4 * (lane >> 5)) =
             u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
@@ -997,8 +1396,8 @@ hipError_t launch_kv_attention_mfma(const KvAttentionArgs& a, KvKind kind, hipSt
     P.a = a;
     P.G = (uint32_t)(a.H / a.KH);
     const uint32_t ps = a.L.page_size;
-    P.ids = std::min((62 + ps) / ps, 65u) + 1;
-    const bool page8 = ps % 8 == 0 && a.L.stride_token < (int64_t(1) << 27);
+    P.ids = (6 + ps) / ps + 1;               // pages that eight positions can lie in
+    const bool page8 = ps % 8 == 0 && a.L.stride_token < (int64_t(1) << 24);
     if (page8) {
         // ps >= 8, positions below 2^31: with 2^(s-1) < ps <= 2^s, ceil(2^(31+s) / ps) fits 32 bits
         // and mulhi(p, that) >> (s - 1) is the quotient.
@@ -1027,9 +1426,12 @@ hipError_t launch_kv_attention_mfma(const KvAttentionArgs& a, KvKind kind, hipSt
     hipLaunchKernelGGL(kernel, dim3(kKvGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
-    log_launch("kv_attention_join", kKvGroups * row_groups, 1024, "T=%d H=%d", a.T, a.H);
-    hipLaunchKernelGGL(a.D == 64 ? kv_attention_join<64> : kv_attention_join<128>, dim3(kKvGroups, row_groups), dim3(1024),
-                       0, s, P);
+    // Few requests and key heads: their items have many pieces.
+    const bool many = (int64_t)a.L.batch * a.KH < 64;
+    log_launch("kv_attention_join", (kKvGroups - 1) * row_groups, many ? 1024 : 256, "T=%d H=%d", a.T, a.H);
+    hipLaunchKernelGGL(a.D == 64 ? (many ? kv_attention_join<64, 4> : kv_attention_join<64, 1>)
+                                 : (many ? kv_attention_join<128, 4> : kv_attention_join<128, 1>),
+                       dim3(kKvGroups - 1, row_groups), dim3(many ? 1024 : 256), 0, s, P);
     return hipGetLastError();
 }
 
