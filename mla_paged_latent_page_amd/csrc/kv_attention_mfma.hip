@@ -34,7 +34,7 @@ constexpr int STAGES = 4;
 constexpr int PAGE_SLOTS = 128;              // page ids that a wave holds in LDS (pages of less than 8 positions)
 constexpr uint32_t OVER = 384;               // an item counts as so many positions more than it has
 constexpr uint32_t SNAP = 64;                // a cut so close to an end of an item is moved there
-constexpr uint32_t LEAST = 256;              // positions of the smallest share
+constexpr uint32_t LEAST = 128;              // positions of the smallest share
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.0f;               // the reference maximum may lag by 2^8
 constexpr float kNothing = -1e30f;           // the reference of a row that has seen nothing
@@ -136,7 +136,6 @@ __device__ inline Request request_at(const Params& P, uint32_t b)
 struct Item {
     uint32_t b, kh, m;
     uint32_t nt, ns, lo;
-    uint64_t cost;
 };
 
 __device__ inline Item item_at(const Params& P, const Request& r, uint32_t kh, uint32_t m)
@@ -153,7 +152,6 @@ __device__ inline Item item_at(const Params& P, const Request& r, uint32_t kh, u
     it.lo = min(low / TILE, end - 1);        // (hi is at least 1; a tile even if no row sees it)
     it.ns = min((min(a.sinks, low) + TILE - 1) / TILE, it.lo);
     it.nt = it.ns + end - it.lo;
-    it.cost = work_before(r, m + 1) - work_before(r, m);
     return it;
 }
 
@@ -231,13 +229,14 @@ struct Schedule {
         for (uint32_t step = 1u << (31 - __clz((int)r.nm)); step; step >>= 1)
             if (m + step < r.nm && work_before(r, m + step) <= off)
                 m += step;
-        off -= work_before(r, m);
+        const uint64_t done = work_before(r, m), cost = work_before(r, m + 1) - done;
+        off -= done;
         Item it = item_at(P, r, kh, m);
         tile = 0;
         if (off > OVER + SNAP) {
             tile = it.nt;
-            if (it.cost - off > SNAP)
-                tile = min((uint32_t)((double)(off - OVER) * (double)it.nt / (double)(it.cost - OVER)), it.nt);
+            if (cost - off > SNAP)
+                tile = min((uint32_t)((double)(off - OVER) * (double)it.nt / (double)(cost - OVER)), it.nt);
         }
         if (tile == it.nt) {
             tile = 0;
@@ -272,7 +271,7 @@ __device__ inline Request uniform(const Request& r)
 }
 __device__ inline Item uniform(const Item& i)
 {
-    return Item{uniform(i.b), uniform(i.kh), uniform(i.m), uniform(i.nt), uniform(i.ns), uniform(i.lo), uniform(i.cost)};
+    return Item{uniform(i.b), uniform(i.kh), uniform(i.m), uniform(i.nt), uniform(i.ns), uniform(i.lo)};
 }
 
 // ---------------------------------------------------------------------------
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
     auto process = [&](auto narrow, uint32_t tile0, uint32_t tile1) __attribute__((always_inline)) {
         constexpr bool N = decltype(narrow)::value;
         constexpr int KB = N ? 1 : 2;        // blocks of 32 positions of a wave
-        const uint32_t group = N ? wave & 3 : wave, kb0 = N ? wave >> 2 : 0;
+        const uint32_t group = N ? wave >> 1 : wave, kb0 = N ? wave & 1 : 0;
         const uint32_t row0 = it.m * (N ? NARROW : WIDE) + group * 32;
         const bool live = row0 < r.rows;
         const uint32_t my_row = min(row0 + col, r.rows - 1), my_tok = my_row / P.G;
@@ -1426,8 +1425,8 @@ hipError_t launch_kv_attention_mfma(const KvAttentionArgs& a, KvKind kind, hipSt
     hipLaunchKernelGGL(kernel, dim3(kKvGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
-    // Few requests and key heads: their items have many pieces.
-    const bool many = (int64_t)a.L.batch * a.KH < 64;
+    // Fewer items than 64: they have more than four pieces each.
+    const bool many = ((int64_t)a.L.batch + (int64_t)a.T * P.G / WIDE) * a.KH < 64;
     log_launch("kv_attention_join", (kKvGroups - 1) * row_groups, many ? 1024 : 256, "T=%d H=%d", a.T, a.H);
     hipLaunchKernelGGL(a.D == 64 ? (many ? kv_attention_join<64, 4> : kv_attention_join<64, 1>)
                                  : (many ? kv_attention_join<128, 4> : kv_attention_join<128, 1>),
