@@ -58,9 +58,10 @@ __device__ __attribute__((always_inline)) inline void each(F&& f)
 // weighed, those of the first block beside the sums, the others beside the first block of scores; added
 // up one product later; and packed, in groups of 8, when their group's old weights have been used (DB
 // products each).
-template <int NV, int KS, int KB, int DB>
+template <int NV, int KS, int KB, int DB, bool FP8>
 struct Order {
-    static constexpr int TOP = NV >= 16 ? 4 : 2, E = 16 * KB, LAST = NV + KS - 2;
+    static constexpr int HALF = NV >= 16 ? 2 : 1;   // e4m3, two blocks: products beside a block's maximum
+    static constexpr int TOP = FP8 && KB == 2 ? 2 * HALF + 1 : NV >= 16 ? 4 : 2, E = 16 * KB, LAST = NV + KS - 2;
     static constexpr int weighed(int i)      // elements weighed before product i
     {
         return i <= TOP ? 0 : i <= NV ? 16 * (i - TOP) / (NV - TOP) : i >= LAST ? E : 16 + (E - 16) * (i - NV) / (LAST - NV);
@@ -845,6 +846,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
                 o[d][e] = 0.0f;
         float mref = kNothing, l = 0.0f;
         f32x16 s[KB];                        // scores of tile t, then its weights
+        [[maybe_unused]] f32x4 ks[4] = {};   // e4m3: scales of keys
         bf16x8 w8[KB][2];                    // weights of tile t - 1, then of tile t, as operands
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -882,10 +884,10 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
         };
         // Element 4 i + e of block b of a tile's scores is position 32 (kb0 + b) + 8 i + 4 half + e of it.
         // e4m3: the scales of the keys.
-        auto scale_keys = [&](uint32_t x) __attribute__((always_inline)) {
+        auto scale_keys = [&](uint32_t x, int b0, int b1) __attribute__((always_inline)) {
             if constexpr (FP8) {
 #pragma unroll
-                for (int b = 0; b < KB; ++b)
+                for (int b = b0; b < b1; ++b)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const f32x4 f = scales_of(scales_at(x), 0, (kb0 + b) * 4 + i);
@@ -999,16 +1001,21 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
             };
             float y[4], base = 0.0f, f = 1.0f, part[4] = {};
             bool some = false;
-            f32x4 vs = {};
-            auto scale = [&](int e0, int e1) __attribute__((always_inline)) {
+            // e4m3: scales are read two products before their use.
+            f32x4 vs[4 * KB];
+            [[maybe_unused]] auto read_keys = [&](uint32_t at, int g) __attribute__((always_inline)) {
+                ks[g % 4] = scales_of(at, 0, kb0 * 4 + g);
+            };
+            [[maybe_unused]] auto scale = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[g / 4][g % 4 * 4 + k] *= ks[g % 4][k];
+            };
+            auto read_values = [&](int e0, int e1) __attribute__((always_inline)) {
                 if constexpr (FP8)
 #pragma unroll
-                    for (int e = e0; e < e1; e += 4) {
-                        const f32x4 z = scales_of(ks_at, 0, kb0 * 4 + e / 4);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            s[e / 16][e % 16 + k] *= z[k];
-                    }
+                    for (int e = (e0 + 3) / 4 * 4; e < e1; e += 4)
+                        vs[e / 4] = scales_of(vs_at, 1, kb0 * 4 + e / 4);
             };
             auto greatest = [&](int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
@@ -1036,11 +1043,8 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
 #pragma unroll
                 for (int e = e0; e < e1; ++e) {
                     part[e & 3] += s[e / 16][e % 16];
-                    if constexpr (FP8) {
-                        if (e % 4 == 0 || e == e0)
-                            vs = scales_of(vs_at, 1, kb0 * 4 + e / 4);
-                        s[e / 16][e % 16] *= vs[e % 4];
-                    }
+                    if constexpr (FP8)
+                        s[e / 16][e % 16] *= vs[e / 4][e % 4];
                 }
                 if (e1 > e0)
                     asm volatile("" : "+v"(part[0]), "+v"(part[1]), "+v"(part[2]), "+v"(part[3]));
@@ -1053,7 +1057,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
                 asm volatile("" : "+v"(x));   // (here: the compiler would move it all behind the branch below)
                 w8[g / 2][g % 2] = as_bf16x8(x);
             };
-            using Z = Order<NV, KS, KB, DB>;
+            using Z = Order<NV, KS, KB, DB, FP8>;
             each<NP>([&](auto step) __attribute__((always_inline)) {
                 constexpr int i = decltype(step)::value;
                 __builtin_amdgcn_sched_barrier(0);
@@ -1067,8 +1071,25 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
                     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x8[i % READS], q[j % KS], s[b], 0, 0, 0);
                 }
                 x8[(i + READS) % NP % READS] = operand(i + READS);
+                if constexpr (FP8 && KB == 2) {
+                    // The second block's scores are scaled here, the first one's behind its products.
+                    constexpr int H = Z::HALF, PER = 4 / H, END = NV + KS, BY = 8 / KS;
+                    if constexpr (i < H)
+                        each<PER>([&](auto g) { read_keys(ks_at, 4 + i * PER + decltype(g)::value); });
+                    else if constexpr (i < 2 * H)
+                        each<PER>([&](auto g) { scale(4 + (i - H) * PER + decltype(g)::value); });
+                    if constexpr (i >= END && i < END + KS / 2)
+                        each<BY>([&](auto g) { read_keys(scales_at(t + 1), (i - END) * BY + decltype(g)::value); });
+                    else if constexpr (i >= END + KS / 2)
+                        each<BY>([&](auto g) { scale((i - END - KS / 2) * BY + decltype(g)::value); });
+                } else if constexpr (FP8) {
+                    if constexpr (i == 0)
+                        each<4>([&](auto g) { scale(decltype(g)::value); });
+                    if constexpr (i >= NP - 4)
+                        read_keys(scales_at(t + 1), i - NP + 4);
+                }
+                read_values(i + 2 > NP ? Z::E : Z::weighed(i + 1), i + 2 > NP ? Z::E : Z::weighed(i + 2));
                 if constexpr (i < Z::TOP - 1) {
-                    scale(Z::E * i / (Z::TOP - 1) / 4 * 4, Z::E * (i + 1) / (Z::TOP - 1) / 4 * 4);
                     greatest(Z::E * i / (Z::TOP - 1) / 4 * 4, Z::E * (i + 1) / (Z::TOP - 1) / 4 * 4);
                 }
                 if constexpr (i == Z::TOP - 1)
@@ -1121,8 +1142,10 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
         lds_barrier();
         turn(-1);
         bool weighed = false, visible = sees_some(0);   // tiles t - 1 and t
-        if (visible)
+        if (visible) {
             scores(0);
+            scale_keys(0, 0, KB - 1);
+        }
 #pragma unroll
         for (int i = 0; i < READS; ++i)
             x8[i] = as_bf16x8(u32x4{0u, 0u, 0u, 0u});
@@ -1137,7 +1160,11 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
             const bool next = plain ? live : t + 1 < n && sees_some(t + 1);
             if (weighed || visible || next) {
                 if (!plain) {
-                    scale_keys(t);
+                    scale_keys(t, KB - 1, KB);
+                    if constexpr (FP8 && KB == 1)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ks[k] = f32x4{1.0f, 1.0f, 1.0f, 1.0f};
                     mask(t, visible);
                     // the operands of tile t - 1 are gone behind this, so what it lacks is added first
                     if (weighed && ragged(tile_start(t - 1)) && uniform(flags[(t - 1) & 3]) == sequence + t - 1)
