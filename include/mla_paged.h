@@ -938,7 +938,8 @@ mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uin
 
 /*
  * kv_attention_paged on an e4m3 cache: K_k[c] and V_k[c] = code * scale of the block of 128
- * columns of the token row that holds the column.
+ * columns of the token row that holds the column.  A scale of values that is not finite makes its
+ * block's columns NaN or infinite for the tokens that see the row.
  *
  * q, out          bf16
  * cache           dtype F8E4M3FN

@@ -223,7 +223,9 @@ template <KvKind KIND, int L, int HEADS>
 hipError_t launch_general(const KvAttentionArgs& a, hipStream_t s)
 {
     const int64_t parts = (a.H / a.KH + HEADS - 1) / HEADS, blocks = (int64_t)a.T * a.KH * parts;
-    const bool many = blocks <= 1024;   // few blocks: more waves for each
+    // Few blocks: more waves for each.  16 against 4 waves: 96 blocks of 2,000 binary32 rows 33 against 63 us, 1,152 of
+    // them 288 against 294, 4,800 blocks of 500 rows 173 against 124.
+    const bool many = blocks <= 1024;
     auto* kernel = many ? kv_attention_general<KIND, L, HEADS, 16> : kv_attention_general<KIND, L, HEADS, 4>;
     const unsigned threads = many ? 1024 : 256;
     // A launch holds less than 2^32 threads in a dimension, and drops those past them without an error.
@@ -241,7 +243,9 @@ hipError_t launch_general(const KvAttentionArgs& a, hipStream_t s)
 template <KvKind KIND>
 hipError_t launch_kind(const KvAttentionArgs& a, hipStream_t s)
 {
-    const bool shared = a.H > a.KH;   // several query heads read the rows of one key head
+    // Several query heads read the rows of one key head: four at a time in a block against one, 64 tokens x 16 heads on
+    // 4 key heads of 80 columns, 2,000 bf16 rows, 80 against 154 us; 32 on 8 of 128, 1,000 binary32 rows, 139 against 295.
+    const bool shared = a.H > a.KH;
     if (a.D <= 64)
         return shared ? launch_general<KIND, 8, 4>(a, s) : launch_general<KIND, 8, 1>(a, s);
     if (a.D <= 128)

@@ -7,16 +7,41 @@
 // one query row throughout: its maximum, sum and rescaling need no exchange but one swap of the wave's
 // halves, and P goes from the score layout into the next product's operand as it is.  The reference
 // is the running maximum, let lag by up to 2^8 (the weights stay below 2^8 in binary32), so the sums
-// are rescaled only now and then.  Weights are rounded to bf16 for the product, their sum is not.
+// are rescaled only now and then.  Weights are rounded to bf16 for the product (2^-8 of each at most,
+// which the output's own rounding may cost too), their sum is not.
 //
-// A workgroup is eight waves, two per SIMD, so that one's softmax runs under the other's products.
-// It takes tiles of 64 positions, loaded into a ring in LDS.  Requests of more than 128 rows have
-// items of 256 rows, 32 per wave; the others one item of up to 128, whose positions two groups of
-// four waves share.
+// A workgroup is eight waves, two per SIMD, and takes tiles of 64 positions.  Requests of more than 128 rows
+// have items of 256 rows, 32 to a wave, which takes both blocks of 32 positions of a tile; the others have one item
+// of up to 128, whose tiles two waves to 32 rows share, on different SIMDs.  (Short items throughout: prompt chunks 0.68 against 0.54 ms, each row of
+// the cache is read and taken from LDS twice as often; long ones throughout: long e4m3 contexts with 20 rows an item 0.42
+// against 0.33 ms, all products in one wave.)
 //
-// Work: every workgroup takes an equal share of the estimated work of all items; shares that end
-// inside an item leave their sums, maximum and sum in the workspace in binary32, and kv_attention_join
-// adds them up in a fixed order.
+// A step t does the products of the sums of tile t - 1 and of the scores of tile t + 1, which do not wait for the
+// softmax of tile t between them: a matrix instruction takes 32 cycles of its pipe, and five or six vector
+// instructions fit beside one, in an order laid down by hand with fences (prompt
+// chunks 0.62 to 0.56 ms).  Operands come from LDS four products ahead, across
+// the step's one barrier too.  Tiles are loaded into LDS rings four steps ahead (bf16) without passing registers, in parts
+// spread over the products.  e4m3 codes go there six steps ahead, each wave converts its eighth of a tile
+// to bf16 (exactly) into a second ring, and the scales multiply scores (keys) and weights (values, behind
+// their sum); they are read two products before their use, without which every group of four waits for LDS (long
+// contexts 0.38 against 0.335 ms, windows 0.82 against 0.72).
+//
+// Steps whose tiles all rows see whole and whose loads are all whole ("plain" ones) skip masks and bounds. Values that
+// are not finite in a tile that some row does not see whole (0 times them would be NaN) are cleared in LDS and added
+// for the rows that see them.
+//
+// Work: every workgroup takes an equal share of the estimated work of all items, in an order that gives
+// neighbouring shares one XCD's L2; shares that end inside an item leave their sums, maximum and sum in the workspace
+// in binary32, and kv_attention_join adds them up in a fixed order.
+//
+// Measured (MI355X; 8 key heads of 128 columns): 5 prompt chunks of 1,000 to 4,096 tokens x 32 heads behind
+// 1 to 8,000 cached rows, bf16, 0.54 ms = 835 TFLOP/s, where an 8192^3 library product reaches 1255.  The products alone would
+// take 0.43 ms in this form; the rest is what lies between items (setup, first loads, results: 8 us
+// each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, which is
+// what a large copy reaches.  6 requests x 40 heads over 60 to 131 thousand rows, e4m3: 0.335 ms, 3.4 TB/s: with at
+// most 20 rows an item, two waves do all products, and the chain of their step bounds it (the loads and
+// conversions alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 ms = 715 TFLOP/s, bound by the issue
+// of conversions, scalings and the softmax beside the products.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -32,9 +57,12 @@ constexpr int TILE = 64;                     // positions of a step
 constexpr int WIDE = 256, NARROW = 128;      // rows of an item
 constexpr int STAGES = 4;
 constexpr int PAGE_SLOTS = 128;              // page ids that a wave holds in LDS (pages of less than 8 positions)
-constexpr uint32_t OVER = 384;               // an item counts as so many positions more than it has
-constexpr uint32_t SNAP = 64;                // a cut so close to an end of an item is moved there
-constexpr uint32_t LEAST = 128;              // positions of the smallest share
+// An item counts as so many positions more than it has: what its start and end cost.  192, 256, 384, 512: prompt
+// chunks 0.61, 0.58, 0.55, 0.55 ms, single tokens 0.49, 0.49, 0.49, 0.50.
+constexpr uint32_t OVER = 384;
+// Positions of the smallest share: 128 against 256 takes four requests of at most 1,000 rows from 25.5 to 22 us, 64
+// no further.
+constexpr uint32_t LEAST = 128;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.0f;               // the reference maximum may lag by 2^8
 constexpr float kNothing = -1e30f;           // the reference of a row that has seen nothing
@@ -234,11 +262,8 @@ struct Schedule {
         off -= done;
         Item it = item_at(P, r, kh, m);
         tile = 0;
-        if (off > OVER + SNAP) {
-            tile = it.nt;
-            if (cost - off > SNAP)
-                tile = min((uint32_t)((double)(off - OVER) * (double)it.nt / (double)(cost - OVER)), it.nt);
-        }
+        if (off > OVER)
+            tile = min((uint32_t)((double)(off - OVER) * (double)it.nt / (double)(cost - OVER)), it.nt);
         if (tile == it.nt) {
             tile = 0;
             it = next(r, it);
@@ -981,9 +1006,9 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
             }
         };
 
-        // The products of a step, of 32 cycles each, with the softmax between
-        // them, five or six other instructions to a product.  The scores' first block is free, and taken by the next
-        // tile's, once its weights are operands.
+        // The products of a step, of 32 cycles each, with the softmax between them, five or six other
+        // instructions to a product.  The scores' first block is free, and taken by the next tile's, once its weights
+        // are operands.
         auto whole_step = [&](uint32_t t, bool plain) __attribute__((always_inline)) {
             const uint32_t vt = Y::values_at((int)t - 1) + kb0 * 32 * Y::ROW + v0;
             const uint32_t vn = Y::values_at((int)t) + kb0 * 32 * Y::ROW + v0;
@@ -1452,7 +1477,9 @@ hipError_t launch_kv_attention_mfma(const KvAttentionArgs& a, KvKind kind, hipSt
     hipLaunchKernelGGL(kernel, dim3(kKvGroups), dim3(64 * WAVES), 0, s, P);
     if (hipError_t e = hipGetLastError())
         return e;
-    // Fewer items than 64: they have more than four pieces each.
+    // Fewer items than 64: they have more than four pieces each.  Four groups of waves against one: one token of 8 heads on
+    // a key head behind 131,071 rows (256 pieces) 69 against 118 us, of 32 on 8 behind 32,767 43 against 49; prompt
+    // chunks (2 or 3 pieces) 551 against 536.
     const bool many = ((int64_t)a.L.batch + (int64_t)a.T * P.G / WIDE) * a.KH < 64;
     log_launch("kv_attention_join", (kKvGroups - 1) * row_groups, many ? 1024 : 256, "T=%d H=%d", a.T, a.H);
     hipLaunchKernelGGL(a.D == 64 ? (many ? kv_attention_join<64, 4> : kv_attention_join<64, 1>)
