@@ -854,7 +854,8 @@ mla_status_t kv_write_paged(const void* k, const void* v, int64_t k_stride_token
  * columns of the K row and of the V row:
  *   amax = max |y| of the block, s = amax / 448 (1 for a block of zeros)
  *   codes = e4m3fn(y * (448 / amax)), round to nearest even; s into the scale pool
- * An amax below 448 * 2^-126 counts as that.
+ * An amax below 448 * 2^-126 counts as that.  NaN does not count for amax and becomes the code of
+ * NaN; an infinity makes its block's scale infinite.
  *
  * cache           dtype F8E4M3FN, num_heads*head_dim % 16 == 0; pages are WRITTEN
  * cache_scales    [host] granularity 128, stride_token >= ceil(num_heads*head_dim / 128),
@@ -939,7 +940,7 @@ mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uin
 /*
  * kv_attention_paged on an e4m3 cache: K_k[c] and V_k[c] = code * scale of the block of 128
  * columns of the token row that holds the column.  A scale of values that is not finite makes its
- * block's columns NaN or infinite for the tokens that see the row.
+ * block's columns NaN or infinite for the tokens that see the row; finite ones are to stay below 2^119.
  *
  * q, out          bf16
  * cache           dtype F8E4M3FN

@@ -1435,8 +1435,10 @@ __global__ void __launch_bounds__(256 * SETS) kv_attention_join(Params P)
 
 bool kv_attention_mfma_fits(const KvAttentionArgs& a, KvKind kind)
 {
-    // (the kernel's scale is in units of log2, and divides)
-    return kind != KV_F32 && (a.D == 64 || a.D == 128) && std::isnormal(a.scale * kLog2e) &&
+    // The kernel's references are scores before scaling.  With a scale below 2^-64 these could lie below kNothing, and
+    // with one above 2^26 kNothing times it could be infinite.
+    const float c = std::fabs(a.scale) * kLog2e;
+    return kind != KV_F32 && (a.D == 64 || a.D == 128) && c >= 0x1p-64f && c <= 0x1p26f &&
            // items are numbered in 32 bits, and their work together in 64
            (uint64_t)a.L.batch * a.KH < (uint64_t(1) << 24);
 }

@@ -71,6 +71,49 @@ def test_what_a_token_does_not_see_may_hold_anything(lens, new, G, window, sinks
     assert bool(((z.double() - zref).abs() <= ltol)[~zhit].all())
 
 
+@pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "bf16"), (80, "bf16"), (64, "f32")])
+def test_infinite_scores(D, dtype):
+    # a key of +infinity in one column: heads whose query is positive there have a score of +infinity, the others
+    # one of -infinity, a weight of 0
+    at = 150
+    case = KvCase(60, [140], [70], 8, 2, D, dtype=dtype)
+    flip = torch.arange(8, device="cuda") % 2 * 2 - 1
+    case.q[:, :, 3] = (case.q[:, :, 3].abs() + 0.1) * flip
+    page, slot = case.where(0, [at])
+    sees = case.seen(0)[:, at]
+    hidden = case.seen(0)
+    clean = case.reference()
+    hidden[:, at] = False
+    case.seen = lambda b: hidden
+    without = case.reference()
+    case.dev.pool[int(page[0]), 1, 0, int(slot[0]), :, 3] = math.inf
+    out, z = attend(case)
+    lost = sees[:, None] & (flip > 0)
+    assert not bool(torch.isfinite(out[lost]).any()) and not bool(torch.isfinite(z[lost]).any())
+    for (ref, zref, tol, ltol), rows in ((clean, ~sees[:, None] & (flip != 0)), (without, sees[:, None] & (flip < 0))):
+        assert bool(((out.double() - ref).abs() <= tol)[rows].all())
+        assert bool(((z.double() - zref).abs() <= ltol)[rows].all())
+
+
+def test_written_values_that_are_not_finite():
+    case = KvCase(61, [4], [3], 2, 2, 128, dtype="e4m3")
+    g = torch.Generator(device="cuda").manual_seed(61)
+    k, v = (torch.randn((3, 2, 128), generator=g, device="cuda").to(BF16) for _ in range(2))
+    want = k.clone()
+    k[0, 0, 3], k[1, 0, 3], k[1, 1, 5], v[2] = math.nan, math.inf, -math.inf, math.nan
+    want[0, 0, 3] = 0
+    mp.kv_write_paged_fp8(k, v, case.iro, cache_of(case), 1)
+    page, slot = case.where(0, range(4, 7))
+    codes, scales = quantised(want.double().view(3, 256))
+    got, sc = case.dev.pool[page, 1, 0, slot].view(3, 256), case.dev.scales[page, 1, 0, slot]
+    keep = torch.ones(256, dtype=torch.bool, device="cuda")
+    keep[3] = False
+    assert same(got[0, keep], codes.view(torch.uint8)[0, keep]) and same(sc[0], scales[0])
+    assert int(got[0, 3]) & 0x7F == 0x7F and bool(torch.isinf(sc[1]).all())
+    assert same(got[2], codes.view(torch.uint8)[2]) and same(sc[2], scales[2])
+    assert bool((case.dev.pool[page, 1, 1, slot][2] & 0x7F == 0x7F).all())
+
+
 # ---------------------------------------------------------------------------
 # shares, joins, shapes
 # ---------------------------------------------------------------------------
@@ -106,6 +149,30 @@ def test_scales_of_either_sign(scale, D, dtype):
     case = KvCase(9, [300, 20], [5, 90], 8, 2, D, dtype=dtype, q_std=0.25 if abs(scale) == 1 else 1.0)
     case.scale = scale
     check_kv_attention(case, *attend(case))
+
+
+@pytest.mark.parametrize("D, dtype, q, k, scale", [(128, "bf16", 2.0 ** 50, 2.0 ** 50, 2.0 ** -104),
+                                                  (64, "bf16", 2.0 ** 40, 2.0 ** 23, 2.0 ** -66),
+                                                  (64, "bf16", 2.0 ** 40, 2.0 ** 21, -2.0 ** -64),
+                                                  (128, "bf16", 2.0 ** -14, 2.0 ** -13, 2.0 ** 25),
+                                                  (64, "bf16", 2.0 ** -14, 2.0 ** -13, -2.0 ** 27),
+                                                  (128, "bf16", 2.0 ** -45, 2.0 ** -45, 2.0 ** 86)])
+def test_small_and_large_scales(D, dtype, q, k, scale):
+    # scores of ordinary size from queries, keys and scales that are not
+    case = KvCase(12, [0, 0, 300, 1], [1, 3, 5, 140], 8, 2, D, dtype=dtype)
+    case.q *= q
+    case.dev.pool[:, :, 0] *= k
+    case.scale = scale
+    check_kv_attention(case, *attend(case))
+
+
+def test_rows_far_apart():
+    # 16 MiB between token rows
+    case = KvCase(13, [40, 3], [3, 90], 8, 2, 128)
+    ref, zref = attend(case)
+    case.dev.pool = apart(case.dev.pool, 4 * 16 * (1 << 23) + 128, (1 << 23) - 256)
+    out, z = attend(case)
+    assert same(out, ref) and same(z, zref)
 
 
 @pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "bf16"), (128, "e4m3"), (80, "f32")])
