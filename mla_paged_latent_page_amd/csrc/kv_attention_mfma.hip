@@ -57,8 +57,8 @@ constexpr int TILE = 64;                     // positions of a step
 constexpr int WIDE = 256, NARROW = 128;      // rows of an item
 constexpr int STAGES = 4;
 constexpr int PAGE_SLOTS = 128;              // page ids that a wave holds in LDS (pages of less than 8 positions)
-// An item counts as so many positions more than it has: what its start and end cost.  192, 256, 384, 512: prompt
-// chunks 0.61, 0.58, 0.55, 0.55 ms, single tokens 0.49, 0.49, 0.49, 0.50.
+// An item counts as so many positions more than it has: what its start and end cost.  256, 384, 512: prompt chunks
+// 0.578, 0.552, 0.551 ms, single tokens 0.497, 0.501, 0.504, long e4m3 contexts 0.447, 0.423, 0.445.
 constexpr uint32_t OVER = 384;
 // Positions of the smallest share: 128 against 256 takes four requests of at most 1,000 rows from 25.5 to 22 us, 64
 // no further.

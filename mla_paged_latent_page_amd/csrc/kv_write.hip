@@ -8,17 +8,22 @@
 //
 // Memory-bound: 4 HD bytes read, 4 HD (bf16) or 2 HD + 8 HD / 128 (e4m3) written per token.  A
 // lane holds 8 columns, 16 lanes a block of 128, so that a block's amax is four DPP steps.  The
-// pieces of all tokens (keys, then values) are one flat run, of which a wave takes 256: four
-// loads in flight per lane before the chain offsets -> length -> page -> store begins, which
+// pieces of all tokens (keys, then values) are one flat run, of which a wave takes 256 (e4m3 128): four
+// loads in flight per lane (two) before the chain offsets -> length -> page -> store begins, which
 // one lane per token walks for the wave (up to nine tokens, their requests counted by ballots).
+// Measured from memory: 16,372 tokens into bf16 pages 33.4 us = 4.3 TB/s, 36,257 into e4m3 pages 61 us = 3.9 TB/s;
+// a large copy reaches 5.1.
 #include "kv.hpp"
 
 namespace mla {
 namespace {
 
-constexpr int U = 4;                  // pieces of a lane
+// Pieces of a lane.  bf16: 4 against 2, 16,372 tokens of 8 heads of 128 columns 23.3 against 24.0 us; e4m3: 2 against 4,
+// 36,257 tokens 56 against 58 us, and 61 against 65 where the inputs come from memory (fewer registers, more waves
+// under the rotation, the divisions and the packing); 1 takes 70.
+template <bool FP8>
+constexpr int kPieces = FP8 ? 2 : 4;
 constexpr int WAVES = 4;
-constexpr int PIECES = 64 * U;        // of a wave
 
 __device__ inline uint64_t shfl64(uint64_t v, int lane)
 {
@@ -29,6 +34,7 @@ __device__ inline uint64_t shfl64(uint64_t v, int lane)
 template <bool FP8, bool HALF>
 __global__ void __launch_bounds__(64 * WAVES) kv_write_kernel(KvWriteArgs a, uint32_t first_token, uint32_t tokens)
 {
+    constexpr int U = kPieces<FP8>, PIECES = 64 * U;   // of a lane, of a wave
     const int lane = threadIdx.x & 63;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t nblk = (a.HD + 127) / 128, per_half = nblk * 16, per_token = 2 * per_half;
@@ -172,10 +178,10 @@ hipError_t launch_kv_write(const KvWriteArgs& a, bool fp8, bool half, hipStream_
                        : (half ? kv_write_kernel<false, true> : kv_write_kernel<false, false>);
     // Pieces of a launch are numbered in 32 bits.
     const int64_t per_token = 2 * ((a.HD + 127) / 128) * 16;
-    const int64_t most = (int64_t(1) << 30) / per_token;
+    const int64_t most = (int64_t(1) << 30) / per_token, per_block = 64 * WAVES * (fp8 ? kPieces<true> : kPieces<false>);
     for (int64_t first = 0; first < a.T; first += most) {
         const int64_t tokens = a.T - first < most ? a.T - first : most;
-        const unsigned grid = (unsigned)((tokens * per_token + PIECES * WAVES - 1) / (PIECES * WAVES));
+        const unsigned grid = (unsigned)((tokens * per_token + per_block - 1) / per_block);
         log_launch(fp8 ? "kv_write_kernel<e4m3>" : "kv_write_kernel<bf16>", grid, 64 * WAVES, "T=%d HD=%d R=%d half=%d",
                    a.T, a.HD, a.R, (int)half);
         hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), 0, s, a, (uint32_t)first, (uint32_t)tokens);
