@@ -143,6 +143,48 @@ def test_shares_and_joins(lens, new, H, KH, D, page_size, window, sinks, dtype):
     assert same(out, again) and same(z, z2)
 
 
+@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (64, "e4m3"), (80, "f32")])
+def test_many_requests(D, dtype):
+    rng = np.random.default_rng(14)
+    lens, new = rng.integers(0, 200, 300), rng.choice([0, 0, 1, 2, 40], 300)
+    new[5], new[299] = 70, 1
+    case = KvCase(14, lens, new, 4, 2, D, dtype=dtype)
+    check_kv_attention(case, *attend(case))
+    rows = np.minimum(lens, rng.integers(0, 60, 300))
+    M = int(rows.sum())
+    dt = torch.float32 if dtype == "f32" else BF16
+    kb, vb = torch.empty((M, 2, D), dtype=dt, device="cuda"), torch.empty((M, 2, D), dtype=dt, device="cuda")
+    call = mp.kv_gather_paged_fp8_cache if dtype == "e4m3" else mp.kv_gather_paged
+    call(i32(np.concatenate([[0], np.cumsum(rows)]), "cuda"), i32(lens - rows, "cuda"), M, cache_of(case), 1, kb, vb)
+    for side, got in ((0, kb), (1, vb)):
+        want = torch.cat([case.rows64(b, side, range(n - m, n)) for b, (n, m) in enumerate(zip(lens, rows)) if m])
+        assert same(got, want.float().to(dt))
+
+
+@pytest.mark.parametrize("page_size", [16, 3])
+@pytest.mark.parametrize("D, dtype", [(128, "bf16"), (128, "e4m3"), (64, "e4m3"), (80, "f32")])
+def test_page_ids_past_the_pool_stay_with_their_request(D, dtype, page_size):
+    # reads clamp them: the request's own outputs are unspecified, the others' are not touched
+    case = KvCase(15, [300, 40, 200], [2, 5, 140], 8, 2, D, page_size=page_size, dtype=dtype)
+    ref, zref = attend(case)
+    case.dev.page_table[0, :3] = -1
+    case.dev.page_table[0, 3] = case.dev.pool.shape[0]
+    out, z = attend(case)
+    assert same(out[2:], ref[2:]) and same(z[2:], zref[2:])
+
+
+@pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "e4m3"), (80, "f32")])
+def test_windows_without_effect(D, dtype):
+    # sinks without a window, and a window longer than every context, change nothing
+    case = KvCase(16, [300, 0], [3, 200], 4, 2, D, dtype=dtype)
+    ref, zref = attend(case)
+    case.sinks = 7
+    out, z = attend(case)
+    assert same(out, ref) and same(z, zref)
+    for case.window, case.sinks in ((304, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+        check_kv_attention(case, *attend(case))
+
+
 @pytest.mark.parametrize("scale", [-0.125, 0.0, 2.0 ** -40, -2.0 ** -135, 1.0])
 @pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "e4m3"), (80, "f32")])
 def test_scales_of_either_sign(scale, D, dtype):
