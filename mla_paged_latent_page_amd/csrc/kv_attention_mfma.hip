@@ -35,12 +35,12 @@
 // in binary32, and kv_attention_join adds them up in a fixed order.
 //
 // Measured (MI355X; 8 key heads of 128 columns): 5 prompt chunks of 1,000 to 4,096 tokens x 32 heads behind
-// 1 to 8,000 cached rows, bf16, 0.54 ms = 835 TFLOP/s, where an 8192^3 library product reaches 1255.  The products alone would
+// 1 to 8,000 cached rows, bf16, 0.54 to 0.56 ms = 808 to 846 TFLOP/s, where an 8192^3 library product reaches 1255.  The products alone would
 // take 0.43 ms in this form; the rest is what lies between items (setup, first loads, results: 8 us
 // each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, which is
 // what a large copy reaches.  6 requests x 40 heads over 60 to 131 thousand rows, e4m3: 0.335 ms, 3.4 TB/s: with at
 // most 20 rows an item, two waves do all products, and the chain of their step bounds it (the loads and
-// conversions alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 ms = 715 TFLOP/s, bound by the issue
+// conversions alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 to 0.74 ms = 695 to 715 TFLOP/s, bound by the issue
 // of conversions, scalings and the softmax beside the products.
 #include <algorithm>
 #include <cmath>
@@ -322,8 +322,8 @@ __device__ inline f32x2 halves(float v)
     return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
 }
 
-// lds_barrier() with the last operand reads (READS, of two instructions each) still in flight: what they read
-// is not written in the step that begins here.
+// lds_barrier() with the last operand reads (READS, of two instructions each; or, among them, reads of the next
+// tile's scales) still in flight: what they read is not written in the step that begins here.
 constexpr int READS = 4;                     // products that an operand is read ahead
 __device__ inline void step_barrier()
 {
