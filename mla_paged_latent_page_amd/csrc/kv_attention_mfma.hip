@@ -1,47 +1,45 @@
-// Attention over a paged K/V cache on the matrix cores: heads of 64 or 128 columns, bf16 or e4m3
-// cache (see kv_attention.hip for the operator and the general form).
+// Attention over a paged K/V cache on the matrix cores: heads of 64 or 128 columns, bf16 or e4m3 cache (see
+// kv_attention.hip for the operator and the general form).
 //
-// The query heads that share a key head are rows of one product: row r of a request is token r / G,
-// head r % G.  A wave holds 32 rows and takes 32 cached positions at a time: scores S^T = K Q^T,
-// weights P = exp(S - reference), O^T += V^T P^T (products of 32x32x16).  Transposed like this a lane has
-// one query row throughout: its maximum, sum and rescaling need no exchange but one swap of the wave's
-// halves, and P goes from the score layout into the next product's operand as it is.  The reference
-// is the running maximum, let lag by up to 2^8 (the weights stay below 2^8 in binary32), so the sums
-// are rescaled only now and then.  Weights are rounded to bf16 for the product (2^-8 of each at most,
-// which the output's own rounding may cost too), their sum is not.
+// The query heads that share a key head are rows of one product: row r of a request is token r / G, head r % G.  A
+// wave holds 32 rows and takes 32 cached positions at a time: scores S^T = K Q^T, weights P = exp(S - reference),
+// O^T += V^T P^T (products of 32x32x16).  Transposed like this a lane has one query row throughout: its maximum, sum
+// and rescaling need no exchange but one swap of the wave's halves, and P goes from the score layout into the next
+// product's operand as it is.  The reference is the running maximum, let lag by up to 2^8 (the weights stay below
+// 2^8 in binary32), so the sums are rescaled only now and then.  Weights are rounded to bf16 for the product (2^-8
+// of each at most, which the output's own rounding may cost too), their sum is not.
 //
-// A workgroup is eight waves, two per SIMD, and takes tiles of 64 positions.  Requests of more than 128 rows
-// have items of 256 rows, 32 to a wave, which takes both blocks of 32 positions of a tile; the others have one item
-// of up to 128, whose tiles two waves to 32 rows share, on different SIMDs.  (Short items throughout: prompt chunks 0.68 against 0.54 ms, each row of
-// the cache is read and taken from LDS twice as often; long ones throughout: long e4m3 contexts with 20 rows an item 0.42
-// against 0.33 ms, all products in one wave.)
+// A workgroup is eight waves, two per SIMD, and takes tiles of 64 positions.  Requests of more than 128 rows have
+// items of 256 rows, 32 to a wave, which takes both blocks of 32 positions of a tile; the others have one item of
+// up to 128, whose tiles two waves to 32 rows share, on different SIMDs.  (Short items throughout: prompt chunks
+// 0.68 against 0.54 ms, each row of the cache is read and taken from LDS twice as often; long ones throughout: long
+// e4m3 contexts with 20 rows an item 0.42 against 0.33 ms, all products in one wave.)
 //
 // A step t does the products of the sums of tile t - 1 and of the scores of tile t + 1, which do not wait for the
 // softmax of tile t between them: a matrix instruction takes 32 cycles of its pipe, and five or six vector
-// instructions fit beside one, in an order laid down by hand with fences (prompt
-// chunks 0.62 to 0.56 ms).  Operands come from LDS four products ahead, across
-// the step's one barrier too.  Tiles are loaded into LDS rings four steps ahead (bf16) without passing registers, in parts
-// spread over the products.  e4m3 codes go there six steps ahead, each wave converts its eighth of a tile
-// to bf16 (exactly) into a second ring, and the scales multiply scores (keys) and weights (values, behind
-// their sum); they are read two products before their use, without which every group of four waits for LDS (long
-// contexts 0.38 against 0.335 ms, windows 0.82 against 0.72).
+// instructions fit beside one, in an order laid down by hand with fences (prompt chunks 0.62 to 0.56 ms).  Operands
+// come from LDS four products ahead, across the step's one barrier too.  Tiles are loaded into LDS rings four steps
+// ahead (bf16) without passing registers, in parts spread over the products.  e4m3 codes go there six steps ahead,
+// each wave converts its eighth of a tile to bf16 (exactly) into a second ring, and the scales multiply scores
+// (keys) and weights (values, behind their sum); they are read two products before their use, without which every
+// group of four waits for LDS (long contexts 0.38 against 0.335 ms, windows 0.82 against 0.72).
 //
-// Steps whose tiles all rows see whole and whose loads are all whole ("plain" ones) skip masks and bounds. Values that
-// are not finite in a tile that some row does not see whole (0 times them would be NaN) are cleared in LDS and added
-// for the rows that see them.
+// Steps whose tiles all rows see whole and whose loads are all whole ("plain" ones) skip masks and bounds. Values
+// that are not finite in a tile that some row does not see whole (0 times them would be NaN) are cleared in LDS and
+// added for the rows that see them.
 //
 // Work: every workgroup takes an equal share of the estimated work of all items, in an order that gives
-// neighbouring shares one XCD's L2; shares that end inside an item leave their sums, maximum and sum in the workspace
-// in binary32, and kv_attention_join adds them up in a fixed order.
+// neighbouring shares one XCD's L2; shares that end inside an item leave their sums, maximum and sum in the
+// workspace in binary32, and kv_attention_join adds them up in a fixed order.
 //
-// Measured (MI355X; 8 key heads of 128 columns): 5 prompt chunks of 1,000 to 4,096 tokens x 32 heads behind
-// 1 to 8,000 cached rows, bf16, 0.54 to 0.56 ms = 808 to 846 TFLOP/s, where an 8192^3 library product reaches 1255.  The products alone would
-// take 0.43 ms in this form; the rest is what lies between items (setup, first loads, results: 8 us
-// each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, which is
+// Measured (MI355X; 8 key heads of 128 columns): 5 prompt chunks of 1,000 to 4,096 tokens x 32 heads behind 1 to
+// 8,000 cached rows, bf16, 0.54 to 0.56 ms = 808 to 846 TFLOP/s, where an 8192^3 library product reaches 1255.  The
+// products alone would take 0.43 ms in this form; the rest is what lies between items (setup, first loads, results:
+// 8 us each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, which is
 // what a large copy reaches.  6 requests x 40 heads over 60 to 131 thousand rows, e4m3: 0.335 ms, 3.4 TB/s: with at
-// most 20 rows an item, two waves do all products, and the chain of their step bounds it (the loads and
-// conversions alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 to 0.74 ms = 695 to 715 TFLOP/s, bound by the issue
-// of conversions, scalings and the softmax beside the products.
+// most 20 rows an item, two waves do all products, and the chain of their step bounds it (the loads and conversions
+// alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 to 0.74 ms = 695 to 715 TFLOP/s, bound by the
+// issue of conversions, scalings and the softmax beside the products.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
