@@ -1164,6 +1164,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
         ready(-1);
         lds_barrier();
         turn(-1);
+        wait_lds();                          // (a wave that sees nothing of the first tile reads nothing before the barrier)
         bool weighed = false, visible = sees_some(0);   // tiles t - 1 and t
         if (visible) {
             scores(0);

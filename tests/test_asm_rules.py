@@ -1,0 +1,51 @@
+"""Waits that inline assembly needs, in the generated code of the kernels that use it (tests/asm_rules.py)."""
+import os
+
+import pytest
+
+from asm_rules import generated, kernels, pending_stores
+from mla_paged_latent_page_amd import build as B
+
+needs_hipcc = pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="no hipcc")
+
+
+def one(text):
+    (code,) = kernels("_Z1k:\n" + text + "\ts_endpgm\n.Lfunc_end0:\n").values()
+    return code
+
+
+def written(text):
+    return "\t;;#ASMSTART\n" + text + "\t;;#ASMEND\n"
+
+
+STORE, READ = "\tds_write_b128 v0, v[4:7]\n", "\tds_read_b128 v[8:11], v1\n"
+BARRIER8 = written("\ts_waitcnt lgkmcnt(8)\n\ts_barrier\n")
+
+
+@pytest.mark.parametrize("text, any_wait, written_wait", [
+    (STORE + BARRIER8, 1, 1),                                                    # the wait is missing
+    (STORE + 7 * READ + BARRIER8, 1, 1),
+    (STORE + 8 * READ + BARRIER8, 0, 0),                                         # reads behind it push it out
+    (STORE + written("\ts_waitcnt lgkmcnt(0)\n") + BARRIER8, 0, 0),
+    (STORE + "\ts_waitcnt lgkmcnt(0)\n" + BARRIER8, 0, 1),                       # a wait of the compiler's
+    (STORE + "\ts_waitcnt vmcnt(0)\n" + BARRIER8, 1, 1),
+    (STORE + "\ts_cbranch_vccz .LBB0_1\n" + 8 * READ + ".LBB0_1:\n" + BARRIER8, 1, 1),     # one path lacks them
+    (".LBB0_1:\n" + BARRIER8 + STORE + "\ts_cbranch_scc1 .LBB0_1\n", 1, 1),      # round a loop
+    (STORE + "\ts_waitcnt lgkmcnt(0)\n\ts_barrier\n", 0, 0),                     # __syncthreads
+])
+def test_pending_stores_are_seen(text, any_wait, written_wait):
+    assert len(pending_stores(one(text))) == any_wait
+    assert len(pending_stores(one(text), written_waits=True)) == written_wait
+
+
+@needs_hipcc
+def test_no_store_into_lds_is_pending_at_a_barrier():
+    found = generated("kv_attention_mfma.hip")
+    main = {k: v for k, v in found.items() if "kv_attention_mfma" in k}
+    assert len(main) == 8 and len(found) > 8
+    for name, code in found.items():
+        assert not pending_stores(code), name
+    for name, code in main.items():
+        assert sum(x.op.startswith("ds_write") for x in code) > 10 and sum(x.op == "s_barrier" for x in code) > 8
+        bad = pending_stores(code, written_waits=True)
+        assert not bad, (name, bad[:3])
