@@ -155,10 +155,11 @@ __device__ inline uint32_t lds_addr(const void* p)
 // 16 bytes per lane from memory into LDS at lds + 16 * lane, issued from inline
 // assembly: the compiler does not know this instruction writes LDS, so it adds
 // no waits of its own for it.  The caller orders it against LDS reads with
-// explicit s_waitcnt vmcnt and barriers.
+// explicit s_waitcnt vmcnt and barriers.  A load into LDS takes its destination
+// from m0 and needs a wait state behind the write of it (tests/test_asm_rules.py).
 __device__ inline void asm_ld16_lds(i32x4 srd, uint32_t lds, uint32_t voff, uint32_t soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(srd), "s"(soff)
                  : "memory", "m0");
@@ -167,7 +168,7 @@ __device__ inline void asm_ld16_lds(i32x4 srd, uint32_t lds, uint32_t voff, uint
 // 4 bytes per lane from memory into LDS at lds + 4 * lane (same rules as above).
 __device__ inline void asm_ld4_lds(i32x4 srd, uint32_t lds, uint32_t voff, uint32_t soff)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(srd), "s"(soff)
                  : "memory", "m0");
@@ -177,7 +178,7 @@ __device__ inline void asm_ld4_lds(i32x4 srd, uint32_t lds, uint32_t voff, uint3
 // from inline assembly (same rules as asm_ld16_lds).
 __device__ inline void asm_gld16_lds(const void* src, uint32_t lds)
 {
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
                  : "s"(lds), "v"(src)
                  : "memory", "m0");

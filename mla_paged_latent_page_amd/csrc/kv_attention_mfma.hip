@@ -362,7 +362,7 @@ __device__ inline void load_lds16(const char* base, uint32_t voff, uint32_t lds)
 {
     base = reinterpret_cast<const char*>(uniform(reinterpret_cast<uint64_t>(base)));
     lds = uniform(lds);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");

@@ -288,9 +288,9 @@ __device__ inline float swap32(float v)
 // N loads of 16 bytes per lane into LDS, load j from 128 j bytes past the lane's address to
 // lds + j * BLOCK_BYTES + 16 * lane (the instruction's offset moves both), by the lanes of the
 // masks lo and hi; from a uniform base and a 32-bit lane offset, or from a lane address.  One
-// piece of assembly, as the masks are the whole wave's.
+// piece of assembly, as the masks are the whole wave's.  A wait state lies between a write of m0 and a load.
 #define MLA_LOAD(addr, offset) "global_load_lds_dwordx4 " addr " offset:" offset "\n\t"
-#define MLA_NEXT "s_add_u32 m0, m0, 3968\n\t"
+#define MLA_NEXT "s_add_u32 m0, m0, 3968\n\ts_nop 0\n\t"
 #define MLA_LOADS(N, addr)                                                                                        \
     if constexpr (J == 0 && N == 3)                                                                               \
         asm volatile(MLA_ON MLA_LOAD(addr, "0") MLA_NEXT MLA_LOAD(addr, "128") MLA_NEXT MLA_LOAD(addr, "256")     \
@@ -307,7 +307,7 @@ __device__ inline float swap32(float v)
         asm volatile(MLA_ON MLA_LOAD(addr, "256") MLA_NEXT MLA_LOAD(addr, "384") MLA_OFF MLA_ARGS);               \
     else                                                                                                          \
         asm volatile(MLA_ON MLA_LOAD(addr, "0") MLA_OFF MLA_ARGS)
-#define MLA_ON "s_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %0\n\t"
+#define MLA_ON "s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %2\n\ts_mov_b32 exec_hi, %3\n\t"
 #define MLA_OFF "s_mov_b64 exec, -1"
 
 template <int J, int N>

@@ -2,9 +2,11 @@
 follows every path through the branches and returns the places that break it, as (line, text) pairs.
 
 Wait states: one per instruction, N + 1 for s_nop N."""
+import functools
 import os
 import re
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 from mla_paged_latent_page_amd import build as B
 
@@ -68,13 +70,36 @@ def kernels(text):
     return out
 
 
-def generated(name):
-    """The kernels of a source file of the package, compiled with the package's flags."""
-    src = os.path.join(B.SRC_DIR, name)
+def _generated(src):
     r = subprocess.run([B.HIPCC, *B.FLAGS, "-I", os.path.join(B.ROOT, "include"), "--offload-device-only", "-S", "-o", "-",
                         src], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
     return kernels(r.stdout)
+
+
+@functools.lru_cache(maxsize=None)
+def generated():
+    """{source file: its kernels} of the package, compiled with the package's flags."""
+    src = B.sources()
+    with ThreadPoolExecutor(max_workers=8) as ex:
+        return dict(zip(map(os.path.basename, src), ex.map(_generated, src)))
+
+
+def loads_into_lds(code):
+    return [x for x in code if "load_lds" in x.op or x.op.startswith("buffer_load") and re.search(r"\blds\b", x.rest)]
+
+
+def m0_just_written(code):
+    """Loads into LDS with a write of m0, which holds their destination, as the instruction before: one wait state has to
+    lie between them."""
+    def before(x, seen):
+        for y in x.pred:
+            if y.op != "label":
+                yield y
+            elif y not in seen:
+                yield from before(y, seen | {y})
+    return [(x, y) for x in loads_into_lds(code) for y in before(x, frozenset())
+            if y.op.startswith(("s_", "v_")) and y.operands[:1] == ["m0"]]
 
 
 def pending_stores(code, written_waits=False):

@@ -3,7 +3,7 @@ import os
 
 import pytest
 
-from asm_rules import generated, kernels, pending_stores
+from asm_rules import generated, kernels, loads_into_lds, m0_just_written, pending_stores
 from mla_paged_latent_page_amd import build as B
 
 needs_hipcc = pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="no hipcc")
@@ -38,9 +38,39 @@ def test_pending_stores_are_seen(text, any_wait, written_wait):
     assert len(pending_stores(one(text), written_waits=True)) == written_wait
 
 
+LOAD = "\tglobal_load_lds_dwordx4 v4, s[2:3]\n"
+
+
+@pytest.mark.parametrize("text, bad", [
+    ("\ts_mov_b32 m0, s1\n" + LOAD, 1),
+    ("\ts_add_u32 m0, m0, 0x400\n" + LOAD, 1),
+    ("\ts_mov_b32 m0, s1\n\tbuffer_load_dwordx4 v1, s[8:11], s4 offen lds\n", 1),
+    ("\ts_mov_b32 m0, s1\n.LBB0_1:\n" + LOAD, 1),
+    ("\ts_cbranch_scc1 .LBB0_1\n\ts_mov_b32 m0, s1\n.LBB0_1:\n" + LOAD, 1),
+    ("\ts_mov_b32 m0, s1\n\ts_nop 0\n" + LOAD, 0),
+    ("\ts_mov_b32 m0, s1\n\ts_mov_b64 exec, 0xffff\n" + LOAD, 0),
+    ("\ts_mov_b32 m0, s1\n\tbuffer_load_dwordx4 v[4:7], v1, s[8:11], s4 offen\n", 0),     # into registers
+])
+def test_m0_just_written_is_seen(text, bad):
+    assert len(m0_just_written(one(text))) == bad
+
+
+@needs_hipcc
+def test_m0_is_written_ahead_of_the_loads_that_use_it():
+    seen = set()
+    for source, found in generated().items():
+        for name, code in found.items():
+            if loads_into_lds(code):
+                seen.add(source)
+            bad = m0_just_written(code)
+            assert not bad, (source, name, bad[:3])
+    assert {"absorb.hip", "decompress_bf16_ring.hip", "decompress_fp8_ring.hip", "decompress_small.hip",
+            "kv_attention_mfma.hip", "kv_matmul_ring.hip", "tree_attention_mfma.hip"} <= seen
+
+
 @needs_hipcc
 def test_no_store_into_lds_is_pending_at_a_barrier():
-    found = generated("kv_attention_mfma.hip")
+    found = generated()["kv_attention_mfma.hip"]
     main = {k: v for k, v in found.items() if "kv_attention_mfma" in k}
     assert len(main) == 8 and len(found) > 8
     for name, code in found.items():
