@@ -134,7 +134,9 @@ __device__ inline void buf_ld16_lds(rsrc_t r, void* lds, uint32_t voff, uint32_t
 }
 
 // The same buffer resource as four SGPR words, for inline assembly: base,
-// stride 0, num_records = bytes, raw 32-bit format.
+// stride 0, num_records = bytes, raw 32-bit format.  Memory instructions read an
+// SGPR five wait states behind a vector instruction's write of it; the compiler
+// leaves them for its own loads, not for those in inline assembly.
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 __device__ inline i32x4 make_srd(const void* base, uint32_t bytes)
 {
@@ -144,6 +146,7 @@ __device__ inline i32x4 make_srd(const void* base, uint32_t bytes)
     r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu));
     r[2] = __builtin_amdgcn_readfirstlane((int)bytes);
     r[3] = kRsrcFlags;
+    asm("s_nop 4" : "+s"(r));
     return r;
 }
 // LDS address (byte offset in the workgroup's LDS) of a __shared__ location.

@@ -128,3 +128,48 @@ def pending_stores(code, written_waits=False):
                 least[y] = behind
                 todo.append(y)
     return [x for x in code if x.op == "s_barrier" and (x.inline or not written_waits) and least.get(x, NONE) != NONE]
+
+
+def scalars(text):
+    """Names of the scalar registers that an operand (or operand list) holds."""
+    out = set()
+    for lo, hi in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+        out.update(range(int(lo), int(hi) + 1))
+    out.update(int(n) for n in re.findall(r"\bs(\d+)\b", text))
+    return out | ({"vcc"} if re.search(r"\bvcc", text) else set())
+
+
+def written_by_vector(x):
+    """Scalar registers that a vector instruction writes."""
+    if x.op.startswith(("v_readfirstlane", "v_readlane", "v_cmp_")):
+        return scalars(x.operands[0])
+    if re.match(r"v_(add|sub|subrev|addc|subb|subbrev)_co_|v_div_scale|v_mad_[ui]64", x.op):
+        return scalars(x.operands[1])
+    return set()
+
+
+def written_by_scalar(x):
+    if not x.op.startswith("s_") or x.op.startswith(("s_cmp", "s_bitcmp", "s_cbranch", "s_waitcnt", "s_nop", "s_barrier")):
+        return set()
+    return scalars(x.operands[0]) if x.operands else set()
+
+
+def scalars_just_written(code, states=5):
+    """Memory instructions that read a scalar register which a vector instruction wrote less than 5 wait states before."""
+    bad = []
+    for x in code:
+        if not x.op.startswith(VMEM) or not scalars(x.rest):
+            continue
+        todo, had = [(y, 0, frozenset(scalars(x.rest))) for y in x.pred], set()
+        while todo:
+            y, waited, regs = todo.pop()
+            if waited >= states or (y, waited, regs) in had:
+                continue
+            had.add((y, waited, regs))
+            if written_by_vector(y) & regs:
+                bad.append((x, y))
+                continue
+            regs -= written_by_scalar(y)
+            if regs:
+                todo += [(z, waited + y.states, regs) for z in y.pred]
+    return bad

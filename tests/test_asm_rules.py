@@ -3,7 +3,7 @@ import os
 
 import pytest
 
-from asm_rules import generated, kernels, loads_into_lds, m0_just_written, pending_stores
+from asm_rules import generated, kernels, loads_into_lds, m0_just_written, pending_stores, scalars_just_written
 from mla_paged_latent_page_amd import build as B
 
 needs_hipcc = pytest.mark.skipif(not os.path.exists(B.HIPCC), reason="no hipcc")
@@ -66,6 +66,36 @@ def test_m0_is_written_ahead_of_the_loads_that_use_it():
             assert not bad, (source, name, bad[:3])
     assert {"absorb.hip", "decompress_bf16_ring.hip", "decompress_fp8_ring.hip", "decompress_small.hip",
             "kv_attention_mfma.hip", "kv_matmul_ring.hip", "tree_attention_mfma.hip"} <= seen
+
+
+ADDRESS = "\tv_readfirstlane_b32 s2, v9\n"
+
+
+@pytest.mark.parametrize("text, bad", [
+    (ADDRESS + LOAD, 1),
+    (ADDRESS + "\ts_nop 3\n" + LOAD, 1),
+    (ADDRESS + "\ts_nop 4\n" + LOAD, 0),
+    (ADDRESS + 4 * "\tv_mov_b32_e32 v1, v2\n" + LOAD, 1),
+    (ADDRESS + 5 * "\tv_mov_b32_e32 v1, v2\n" + LOAD, 0),
+    (ADDRESS + "\ts_add_u32 s2, s2, s5\n" + LOAD, 0),            # read and written by a scalar instruction since
+    (ADDRESS + "\ts_add_u32 s3, s2, s5\n" + LOAD, 1),
+    ("\tv_readlane_b32 s3, v9, 4\n" + LOAD, 1),
+    ("\tv_readlane_b32 s4, v9, 4\n" + LOAD, 0),
+    ("\tv_cmp_eq_u32_e64 s[2:3], v1, v2\n" + LOAD, 1),
+    ("\tv_readlane_b32 s11, v9, 4\n\tbuffer_load_dwordx4 v1, s[8:11], s4 offen lds\n", 1),
+    ("\tv_readlane_b32 s4, v9, 4\n\tbuffer_load_dwordx4 v1, s[8:11], s4 offen lds\n", 1),
+    (".LBB0_1:\n" + LOAD + ADDRESS + "\ts_cbranch_scc1 .LBB0_1\n", 1),
+])
+def test_scalars_just_written_are_seen(text, bad):
+    assert len(scalars_just_written(one(text))) == bad
+
+
+@needs_hipcc
+def test_scalar_operands_of_memory_instructions_have_arrived():
+    for source, found in generated().items():
+        for name, code in found.items():
+            bad = scalars_just_written(code)
+            assert not bad, (source, name, bad[:3])
 
 
 @needs_hipcc
