@@ -828,13 +828,14 @@ mla_status_t mla_compact_paged(const uint32_t* accepted, const uint32_t* accepte
  *                         = bf16(k[t][h][c] rotated with freqs_cis[positions[t]]), the others
  *   V row[h*head_dim + c] = bf16(v[t][h][c])
  *   in binary32, round to nearest even; pairs and tables as in mla_rope_q.  No other byte of
- *   the pool is written, cache_lengths is not updated, and tokens without a slot are skipped.
+ *   the pool is written, cache_lengths is not updated, and tokens without a slot, or at or past
+ *   input_row_offsets[batch_size], are skipped.
  *
  * k, v            [device] bf16 [total_tokens][num_heads][head_dim], token t at t * stride
  *                 elements (views into a fused projection are taken as they are); 16-byte
  *                 aligned, strides multiples of 8 elements, >= num_heads*head_dim
  * input_row_offsets [device] uint32 [batch_size+1], [0] = 0, nondecreasing
- * total_tokens    [host] input_row_offsets[batch_size]
+ * total_tokens    [host] T >= input_row_offsets[batch_size] (a step captured with a fixed count has more tokens)
  * positions       [device] uint32 [total_tokens]: the freqs_cis row of each token; NULL: the
  *                 position it is written to.  Past the table: its last row
  * freqs_cis       [device] float [max_seq_len][d_rope], 16-byte aligned; may be NULL when

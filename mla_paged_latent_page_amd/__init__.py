@@ -982,8 +982,9 @@ def _kv_write(k, v, input_row_offsets, cache, layer_idx, positions, freqs_cis, l
 def kv_write_paged(k, v, input_row_offsets, cache: PagedKVCache, layer_idx: int, positions=None, freqs_cis=None,
                    layout: str = "interleaved", stream=None) -> None:
     """Place keys and values ([T, heads, head_dim] bfloat16, views with contiguous heads are taken as they
-    are) behind the cached rows of each request.  With freqs_cis ([max_seq_len, d_rope]) the last d_rope
-    columns of every key head are rotated at positions (None: the position written to)."""
+    are) behind the cached rows of each request; tokens behind the last request are skipped.  With freqs_cis
+    ([max_seq_len, d_rope]) the last d_rope columns of every key head are rotated at positions (None: the
+    position written to)."""
     _kv_write(k, v, input_row_offsets, cache, layer_idx, positions, freqs_cis, layout, stream, False)
 
 

@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(64 * WAVES) kv_write_kernel(KvWriteArgs a, uin
         const uint32_t t = t0 + lane;
         const uint32_t b = cnt == 0 ? 0u : min(cnt, a.L.batch) - 1;
         const uint32_t cached = a.cache_len[b], p = cached + (t - a.iro[b]);
-        // -1: no slot for this position, nothing is stored; nor is it past 2^32
-        off = (uint64_t)(store_offset(a.L, b, p) | -(int64_t)(p < cached));
+        // -1: no slot for this position, nothing is stored; nor is it past 2^32, or behind the last request
+        off = (uint64_t)(store_offset(a.L, b, p) | -(int64_t)(p < cached || t >= a.iro[a.L.batch]));
         if (FP8)
             soff = (uint64_t)store_offset(a.Ls, b, p);
         const uint32_t pr = a.pos ? a.pos[t] : p;
