@@ -903,7 +903,9 @@ mla_status_t kv_gather_paged_fp8_cache(const uint32_t* buffer_row_offsets, const
  *   A token that sees no row (its window lies past the page table) gets zeros and an lse of
  *   -infinity.  Scores, the running maximum and sum, and the output sums are binary32; the
  *   weights are rounded to bf16 for the product with V where the matrix cores do it.  out is
- *   rounded once (round to nearest even).  Scores are to stay below 2^30 in magnitude.
+ *   rounded once (round to nearest even).  Scores are to stay below 2^30 in magnitude.  The output sums are
+ *   divided at the end, and a weight is up to 2^8 while the running maximum lags: they are finite
+ *   while the largest |V| times the rows seen is below 2^119 (in an e4m3 cache 448 times the scale for |V|).
  *
  * What a row that a token does not see holds (NaN and infinities included) does not change
  * that token's output, nor does anything behind a request's last new token.  Of the rows it
@@ -941,7 +943,8 @@ mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uin
 /*
  * kv_attention_paged on an e4m3 cache: K_k[c] and V_k[c] = code * scale of the block of 128
  * columns of the token row that holds the column.  A scale of values that is not finite makes its
- * block's columns NaN or infinite for the tokens that see the row; finite ones are to stay below 2^119.
+ * block's columns NaN or infinite for the tokens that see the row.  Scales of keys are to stay below 2^119,
+ * scales of values below 2^110 divided by the rows seen.
  *
  * q, out          bf16
  * cache           dtype F8E4M3FN

@@ -1,4 +1,5 @@
-"""The paged K/V cache's operators at the edges of what they accept: rows behind the last request."""
+"""The paged K/V cache's operators at the edges of what they accept: rows behind the last request, values near the
+largest that the sums hold."""
 import math
 
 import numpy as np
@@ -7,9 +8,9 @@ import torch
 
 import mla_paged_latent_page_amd as mp
 import workloads as W
-from plain_kv import KvCase
+from plain_kv import KvCase, check_kv_attention
 from plain_step import i32
-from test_gpu_kv_cache import cache_of, same, written
+from test_gpu_kv_cache import attend, cache_of, same, written
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -59,3 +60,37 @@ def test_writes_behind_the_last_request_are_skipped(lens, new, pad, dtype, given
         page, slot = written(case, new)
         changed = not same(raw(want)[page, 1, :, slot], raw(before)[page, 1, :, slot])
         assert changed
+
+
+# ---------------------------------------------------------------------------
+# values near the largest that the sums hold
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("lens, new, H, KH", [([255], [1], 8, 2), ([100, 3], [156, 1], 4, 2)])
+@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (128, "bf16"), (64, "e4m3"), (128, "e4m3"), (80, "bf16"), (80, "e4m3"),
+                                      (64, "f32")])
+def test_values_just_inside_the_limit(lens, new, H, KH, D, dtype):
+    # |V| x rows seen just below 2^119, and scores that grow by just less than the 2^8 that weights may reach while
+    # their reference lags
+    case = KvCase(71, lens, new, H, KH, D, dtype=dtype)
+    rows = int((case.lens + case.new).max())
+    top = 2.0 ** 119 / rows * 0.99
+    case.q.zero_()
+    case.q[:, :, 0] = 1.0
+    case.scale = math.log(2.0)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        page, slot = case.where(b, range(n + m))
+        k = torch.zeros((n + m, KH, D), device="cuda")
+        k[64:, :, 0] = 7.5
+        sign = torch.randint(0, 2, (n + m, KH, D), device="cuda", generator=torch.Generator("cuda").manual_seed(b)) * 2 - 1
+        sign[:, :, :8] = 1
+        if dtype == "e4m3":
+            case.dev.pool[page, 1, 0, slot] = k.to(torch.float8_e4m3fn).view(torch.uint8)
+            case.dev.pool[page, 1, 1, slot] = (448.0 * sign).to(torch.float8_e4m3fn).view(torch.uint8)
+            case.dev.scales[page, 1, 0, slot] = 1.0
+            case.dev.scales[page, 1, 1, slot] = top / 448
+        else:
+            case.dev.pool[page, 1, 0, slot] = k.to(case.dev.pool.dtype)
+            case.dev.pool[page, 1, 1, slot] = (top * sign).to(case.dev.pool.dtype)
+    out, z = attend(case)
+    check_kv_attention(case, out, z)
+    assert bool((out[:, :, :8].double() > top * 0.98).all())
