@@ -1,5 +1,5 @@
 """The paged K/V cache's operators at the edges of what they accept: rows behind the last request, values near the
-largest that the sums hold."""
+largest that the sums hold, calls of several launches."""
 import math
 
 import numpy as np
@@ -8,8 +8,8 @@ import torch
 
 import mla_paged_latent_page_amd as mp
 import workloads as W
-from plain_kv import KvCase, check_kv_attention
-from plain_step import i32
+from plain_kv import KvCase, cast_pool, check_kv_attention, rotated
+from plain_step import U32, i32
 from test_gpu_kv_cache import attend, cache_of, same, written
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +94,122 @@ def test_values_just_inside_the_limit(lens, new, H, KH, D, dtype):
     out, z = attend(case)
     check_kv_attention(case, out, z)
     assert bool((out[:, :, :8].double() > top * 0.98).all())
+
+
+# ---------------------------------------------------------------------------
+# calls in several launches
+# ---------------------------------------------------------------------------
+def paged(shape, layer_dtype, lengths, page_size, scales=None, seed=72):
+    """A pool of one layer for requests of the given capacities, its pages in random order, and (page, slot) of a
+    request's positions."""
+    need = [-(-n // page_size) for n in lengths]
+    order = np.random.default_rng(seed).permutation(sum(need))
+    table = np.zeros((len(need), max(need)), np.int64)
+    for b, at in enumerate(np.cumsum([0] + need[:-1])):
+        table[b, :need[b]] = order[at:at + need[b]]
+    pool = torch.empty((sum(need), 1, 2, page_size, *shape), dtype=layer_dtype, device="cuda")
+    sc = None if scales is None else torch.empty((sum(need), 1, 2, page_size, scales), device="cuda")
+    cache = mp.PagedKVCache(pool, i32(table, "cuda"), torch.zeros(len(need), dtype=torch.int32, device="cuda"), scales=sc)
+    dev = torch.from_numpy(table).cuda()
+
+    def where(b, positions):
+        p = torch.as_tensor(positions, device="cuda")
+        return dev[b, p // page_size], p % page_size
+    return cache, where
+
+
+def test_writes_and_reads_in_several_launches():
+    # rows of 2^20 columns: 4,096 tokens to a launch; the first token of the second one is inside the second request
+    KH, D = 4096, 256
+    seq = [3000, 1099]
+    T = sum(seq)
+    g = torch.Generator(device="cuda").manual_seed(73)
+    k, v = (torch.randn((T, KH, D), generator=g, device="cuda", dtype=BF16) for _ in range(2))
+    cache, where = paged((KH, D), BF16, seq, 64)
+    iro = i32([0, 3000, T], "cuda")
+    mp.kv_write_paged(k, v, iro, cache, 0)
+    for b, first in ((0, 0), (1, 3000)):
+        for lo in range(0, seq[b], 256):
+            hi = min(lo + 256, seq[b])
+            page, slot = where(b, range(lo, hi))
+            for side, x in ((0, k), (1, v)):
+                right = same(cache.pool[page, 0, side, slot], x[first + lo:first + hi])
+                assert right, (b, lo, side)
+    kb, vb = torch.zeros_like(k), torch.zeros_like(v)
+    mp.kv_gather_paged(iro, i32([0, 0], "cuda"), T, cache, 0, kb, vb)
+    for lo in range(0, T, 256):
+        right = same(kb[lo:lo + 256], k[lo:lo + 256]) and same(vb[lo:lo + 256], v[lo:lo + 256])
+        assert right, lo
+
+
+def test_quantising_writes_and_reads_in_several_launches():
+    # ... into an e4m3 cache, rotated at given positions; and reads of more than 8,192 of its rows
+    KH, D = 4096, 256
+    seq = [3000, 1099]
+    T = sum(seq)
+    g = torch.Generator(device="cuda").manual_seed(74)
+    k, v = (torch.randn((T, KH, D), generator=g, device="cuda", dtype=BF16) for _ in range(2))
+    cache, where = paged((KH, D), torch.uint8, seq, 64, scales=KH * D // 128)
+    table = torch.from_numpy(W.rope_table(500, 128)).cuda()
+    pos = np.arange(T) * 7 % 500
+    mp.kv_write_paged_fp8(k, v, i32([0, 3000, T], "cuda"), cache, 0, positions=i32(pos, "cuda"), freqs_cis=table, layout="half")
+    edges = [0, 1, 2999, 3000, 4094, 4095, 4096, 4097, 4098]
+    for t in edges:
+        b = int(t >= 3000)
+        page, slot = where(b, [t - 3000 * b])
+        kr, mag = rotated(k[t:t + 1].double(), table.double()[pos[t]][None], 128, True)
+        for side, ref, mag in ((0, kr, mag), (1, v[t:t + 1].double(), v[t:t + 1].double().abs())):
+            sc = cache.scales[page, 0, side, slot].double()
+            want = ref.view(1, -1, 128).abs().amax(2) / 448
+            assert bool(((sc - want).abs() <= want * 4 * U32).all()), t
+            sc = sc.repeat_interleave(128, 1).view(1, KH, D)
+            got = cast_pool(cache.pool[page, 0, side, slot], "e4m3") * sc
+            # as in test_write: two products and a sum, half a step of the code, half its smallest step
+            tol = mag * 2 * U32 + ref.abs() * 2.0 ** -4 * 1.001 + sc * 2.0 ** -10
+            assert bool(((got - ref).abs() <= tol).all()), (t, side)
+    del k, v
+    M = 2 * T - 4       # 8,194 rows: of the first request, the second, and all but four of both again
+    again = [3000, 1099, 2998, 1097]
+    four = mp.PagedKVCache(cache.pool, cache.page_table[[0, 1, 0, 1]].contiguous(), cache.cache_lengths[[0, 1, 0, 1]].contiguous(),
+                           scales=cache.scales)
+    kb, vb = (torch.zeros((M, KH, D), dtype=BF16, device="cuda") for _ in range(2))
+    mp.kv_gather_paged_fp8_cache(i32(np.concatenate([[0], np.cumsum(again)]), "cuda"), i32([0, 0, 2, 2], "cuda"), M, four, 0,
+                                 kb, vb)
+    for r, b, p in ((0, 0, 0), (2999, 0, 2999), (3000, 1, 0), (4098, 1, 1098), (4099, 0, 2), (7097, 1, 2), (8190, 1, 1095),
+                    (8191, 1, 1096), (8192, 1, 1097), (8193, 1, 1098)):
+        page, slot = where(b, [p])
+        for side, got in ((0, kb), (1, vb)):
+            sc = cache.scales[page, 0, side, slot].repeat_interleave(128, 1).view(1, KH, D)
+            ref = cache.pool[page, 0, side, slot].view(torch.float8_e4m3fn).float() * sc
+            assert same(got[r:r + 1], ref.to(BF16)), (r, side)
+
+
+def test_attention_in_several_launches():
+    # the general form takes 2^23 tokens x key heads in a launch: 2^20 + 5 tokens of 16 heads
+    T, H, D, window = (1 << 20) + 5, 16, 8, 3
+    cache, where = paged((H, D), torch.float32, [T], 1024)
+    g = torch.Generator(device="cuda").manual_seed(75)
+    cache.pool.normal_(generator=g)
+    q = torch.randn((T, H, D), generator=g, device="cuda")
+    out, z = torch.zeros_like(q), torch.zeros((T, H), device="cuda")
+    ws = torch.empty(mp.kv_attention_workspace_size(T, H, H, D), dtype=torch.uint8, device="cuda")
+    mp.kv_attention_paged(q, i32([0, T], "cuda"), 0.5, cache, 0, out, ws, window=window, sinks=1, lse=z)
+    page, slot = where(0, range(T))
+    K, V = (cache.pool[page, 0, side, slot] for side in (0, 1))
+    step = 1 << 17
+    for lo in range(0, T, step):
+        t = torch.arange(lo, min(lo + step, T), device="cuda")
+        at = torch.stack([t - 2, t - 1, t, torch.zeros_like(t)])          # the window, and the sink where it is not in it
+        seen = (at >= 0) & torch.cat([torch.ones_like(at[:3], dtype=torch.bool), (t > 2)[None]])
+        at = at.clamp_min(0)
+        k, v, x = K[at].double(), V[at].double(), q[t].double()
+        s = ((k * x).sum(3) * 0.5).masked_fill(~seen[:, :, None], -math.inf)
+        mags = ((k * x).abs().sum(3) * 0.5).amax(0)
+        ref = torch.logsumexp(s, 0)
+        w = torch.exp(s - ref)
+        o, mag = (w[..., None] * v).sum(0), (w[..., None] * v.abs()).sum(0)
+        # the bounds of tests/plain_kv.py, of four rows
+        ds = mags * (D + 8) * U32
+        tol = mag * (2 * ds + 2.0 ** -20 + 12 * U32)[..., None] + o.abs() * 2 * U32 + 1e-30
+        assert bool(((out[t].double() - o).abs() <= tol).all()), lo
+        assert bool(((z[t].double() - ref).abs() <= ds + 2.0 ** -20 + 12 * U32 + ref.abs() * 2 * U32).all()), lo
