@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_write_kernel(KvWriteArgs a, uin
     const uint32_t j0 = base / per_token, r0 = base - j0 * per_token;
     if (j0 >= tokens)
         return;
-    const uint32_t t0 = first_token + j0;
+    const uint32_t t0 = first_token + j0, end = a.iro[a.L.batch];
 
     // The lane's pieces: token (counted from t0), key or value, columns; its input.
     uint32_t tok[U], col[U], rc[U];
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(64 * WAVES) kv_write_kernel(KvWriteArgs a, uin
         const uint32_t b = cnt == 0 ? 0u : min(cnt, a.L.batch) - 1;
         const uint32_t cached = a.cache_len[b], p = cached + (t - a.iro[b]);
         // -1: no slot for this position, nothing is stored; nor is it past 2^32, or behind the last request
-        off = (uint64_t)(store_offset(a.L, b, p) | -(int64_t)(p < cached || t >= a.iro[a.L.batch]));
+        off = (uint64_t)(store_offset(a.L, b, p) | -(int64_t)(p < cached || t >= end));
         if (FP8)
             soff = (uint64_t)store_offset(a.Ls, b, p);
         const uint32_t pr = a.pos ? a.pos[t] : p;
