@@ -1,5 +1,5 @@
 """The paged K/V cache's operators at the edges of what they accept: rows behind the last request, values near the
-largest that the sums hold, calls of several launches."""
+largest that the sums hold, calls of several launches, positions below 2^31, large pages, thousands of requests."""
 import math
 
 import numpy as np
@@ -9,7 +9,7 @@ import torch
 import mla_paged_latent_page_amd as mp
 import workloads as W
 from plain_kv import KvCase, cast_pool, check_kv_attention, rotated
-from plain_step import U32, i32
+from plain_step import HALF_BF16, U32, i32
 from test_gpu_kv_cache import attend, cache_of, same, written
 
 pytestmark = pytest.mark.gpu
@@ -213,3 +213,149 @@ def test_attention_in_several_launches():
         tol = mag * (2 * ds + 2.0 ** -20 + 12 * U32)[..., None] + o.abs() * 2 * U32 + 1e-30
         assert bool(((out[t].double() - o).abs() <= tol).all()), lo
         assert bool(((z[t].double() - ref).abs() <= ds + 2.0 ** -20 + 12 * U32 + ref.abs() * 2 * U32).all()), lo
+
+
+# ---------------------------------------------------------------------------
+# far positions and large pages
+# ---------------------------------------------------------------------------
+def plain_window(q, K, V, scale, seen):
+    """out, lse and their bounds (tests/plain_kv.py) of q [T, H, D] over rows K, V [n, KH, D], float64."""
+    T, H, D = q.shape
+    G = H // K.shape[1]
+    out, lse, tol, ltol = [], [], [], []
+    for h in range(H):
+        k, v, x = K[:, h // G].contiguous(), V[:, h // G].contiguous(), q[:, h].double()
+        s = ((x @ k.t().contiguous()) * scale).masked_fill(~seen, -math.inf)
+        ds = ((x.abs() @ k.abs().t().contiguous()) * scale).masked_fill(~seen, 0.0).amax(1) * (D + 8) * U32
+        z = torch.logsumexp(s, 1)
+        w = torch.exp(s - z[:, None])
+        o, mag = w @ v, w @ v.abs()
+        many = 3 * seen.sum(1) * U32
+        half = 0.0 if q.dtype == torch.float32 else HALF_BF16
+        out.append(o)
+        lse.append(z)
+        tol.append(mag * (2 * ds + 2.0 ** -20 + many + half)[:, None] + o.abs() * max(half, 2 * U32) * 1.02 + 1e-30)
+        ltol.append(ds + 2.0 ** -20 + many + z.abs() * 2 * U32)
+    return [torch.stack(x, 1) for x in (out, lse, tol, ltol)]
+
+
+@pytest.mark.parametrize("page_size, pages", [(1 << 20, 2047), ((1 << 20) - 24, 2047), (999999, 2147)])
+@pytest.mark.parametrize("D, dtype", [(64, "bf16"), (64, "e4m3"), (80, "bf16")])
+def test_positions_near_the_largest(D, dtype, page_size, pages):
+    # all logical pages of a request are three pages of the pool, its own; new tokens cross into the last page and end
+    # at the last position, below 2^31; a window and two sinks
+    H, KH, window, sinks = 4, 1, 100, 2
+    capacity = page_size * pages
+    assert 2 ** 31 - 2 ** 21 < capacity < 2 ** 31
+    lens, new = [capacity - page_size - 10, capacity - 20], [30, 20]
+    fp8 = dtype == "e4m3"
+    T = sum(new)
+    pool = torch.zeros((6, 1, 2, page_size, KH, D), dtype=torch.uint8 if fp8 else BF16, device="cuda")
+    scales = torch.ones((6, 1, 2, page_size, 1), device="cuda") if fp8 else None
+    table = torch.stack([torch.arange(pages) % 3, 3 + (torch.arange(pages) * 2 + 1) % 3]).int().cuda()
+    cache = mp.PagedKVCache(pool, table, i32(lens, "cuda"), scales=scales)
+    g = torch.Generator(device="cuda").manual_seed(76)
+    iro = i32([0, 30, 50], "cuda")
+    # rows behind the window and at the start, then the new ones by the call
+    rows, at = [], []
+    for b, n in enumerate(lens):
+        p = torch.cat([torch.arange(0, sinks), torch.arange(n - window, n)]).cuda()
+        x = torch.randn((2, len(p), KH, D), generator=g, device="cuda")
+        page, slot = table[b, p // page_size].long(), p % page_size
+        for side in (0, 1):
+            pool[page, 0, side, slot] = x[side].to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x[side].to(BF16)
+        at.append(torch.cat([p, torch.arange(n, n + new[b], device="cuda")]))
+    k, v = (torch.randn((T, KH, D), generator=g, device="cuda").to(BF16) for _ in range(2))
+    (mp.kv_write_paged_fp8 if fp8 else mp.kv_write_paged)(k, v, iro, cache, 0)
+    M = [100 + n for n in new]
+    kb, vb = (torch.empty((sum(M), KH, D), dtype=BF16, device="cuda") for _ in range(2))
+    (mp.kv_gather_paged_fp8_cache if fp8 else mp.kv_gather_paged)(i32([0, M[0], sum(M)], "cuda"),
+                                                                 i32([n - 100 for n in lens], "cuda"), sum(M), cache, 0, kb, vb)
+    q = torch.randn((T, H, D), generator=g, device="cuda").to(BF16)
+    out, z = torch.empty_like(q), torch.empty((T, H), device="cuda")
+    ws = torch.empty(mp.kv_attention_workspace_size(T, H, KH, D), dtype=torch.uint8, device="cuda")
+    (mp.kv_attention_paged_fp8_cache if fp8 else mp.kv_attention_paged)(q, iro, 0.125, cache, 0, out, ws, window=window,
+                                                                       sinks=sinks, lse=z)
+    for b, (n, m) in enumerate(zip(lens, new)):
+        t0 = [0, 30][b]
+        p, own = at[b], slice(t0, t0 + m)
+        page, slot = table[b, p // page_size].long(), p % page_size
+        rows = []
+        for side in (0, 1):
+            r = cast_pool(pool[page, 0, side, slot], dtype)
+            rows.append(r * scales[page, 0, side, slot].double()[:, :, None] if fp8 else r)
+        read = torch.stack([kb, vb])[:, sum(M[:b]):sum(M[:b]) + M[b]].double()
+        assert same(read, torch.stack(rows)[:, sinks:].float().to(BF16).double())
+        if not fp8:
+            assert same(rows[0][-m:], k[own].double()) and same(rows[1][-m:], v[own].double())
+        me = torch.arange(n, n + m, device="cuda")[:, None]
+        seen = (p <= me) & ((me - p < window) | (p < sinks))
+        ref, zref, tol, ltol = plain_window(q[own], rows[0], rows[1], 0.125, seen)
+        assert bool(((out[own].double() - ref).abs() <= tol).all()) and bool(((z[own].double() - zref).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("page_size", [264, 1000, 4104, 1 << 16, 3001])
+@pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "e4m3"), (80, "f32")])
+def test_large_pages(D, dtype, page_size):
+    case = KvCase(77, [page_size - 3, 2 * page_size + 5 if page_size < 10000 else 7, 0], [9, 70, 1], 4, 2, D, page_size=page_size,
+                  dtype=dtype)
+    check_kv_attention(case, *attend(case))
+
+
+def test_thousands_of_requests():
+    rng = np.random.default_rng(78)
+    lens, new = rng.integers(0, 40, 3000), rng.choice([0, 1, 1, 2], 3000)
+    case = KvCase(78, lens, new, 2, 1, 64)
+    check_kv_attention(case, *attend(case))
+
+
+# ---------------------------------------------------------------------------
+# a step captured with a fixed number of tokens
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("D, dtype", [(128, "bf16"), (64, "e4m3"), (80, "bf16")])
+def test_captured_steps_with_fewer_tokens(D, dtype):
+    H, KH, T, fp8 = 8, 2, 24, dtype == "e4m3"
+    case = KvCase(79, [400, 30, 250], [16, 16, 16], H, KH, D, dtype=dtype)
+    base = [400, 30, 250]
+    cache = cache_of(case)
+    table = torch.from_numpy(W.rope_table(600, D)).cuda()
+    g = torch.Generator(device="cuda").manual_seed(79)
+    x = torch.randn((T, H + 2 * KH, D), generator=g, device="cuda").to(BF16)
+    pos, iro = i32(np.zeros(T), "cuda"), i32([0, 8, 16, 24], "cuda")
+    q, out, z = torch.empty((T, H, D), dtype=BF16, device="cuda"), torch.empty((T, H, D), dtype=BF16, device="cuda"), \
+        torch.empty((T, H), device="cuda")
+    ws = torch.empty(mp.kv_attention_workspace_size(T, H, KH, D), dtype=torch.uint8, device="cuda")
+
+    def step(n):
+        mp.mla_rope_q(x[:n, :H], pos[:n], table, q[:n], d_nope=0, layout="half")
+        (mp.kv_write_paged_fp8 if fp8 else mp.kv_write_paged)(x[:n, H:H + KH], x[:n, H + KH:], iro, cache, 1, positions=pos[:n],
+                                                              freqs_cis=table, layout="half")
+        (mp.kv_attention_paged_fp8_cache if fp8 else mp.kv_attention_paged)(q[:n], iro, case.scale, cache, 1, out[:n], ws,
+                                                                           lse=z[:n])
+    case.dev.cache_lengths.copy_(i32(base, "cuda"))
+    before = case.dev.pool.clone()
+    step(T)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(T)
+    for seq in ([1, 1, 1], [8, 8, 8], [0, 3, 2], [10, 0, 0], [0, 0, 0], [1, 14, 1]):
+        n = sum(seq)
+        iro.copy_(i32(np.concatenate([[0], np.cumsum(seq)]), "cuda"))
+        p = np.concatenate([np.arange(m) + b for b, m in zip(base, seq)] + [np.zeros(T - n)])
+        pos.copy_(i32(p, "cuda"))
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        x[n:] = math.nan
+        case.dev.pool.copy_(before)
+        out.fill_(7.0)
+        z.fill_(7.0)
+        if n:
+            step(n)
+        want = [t.clone() for t in (case.dev.pool, out, z)]
+        case.dev.pool.copy_(before)
+        out.fill_(7.0)
+        z.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        unchanged = same(raw(case.dev.pool), raw(want[0]))
+        assert unchanged and same(out, want[1]) and same(z, want[2]), seq
