@@ -11,7 +11,7 @@
 // pieces of all tokens (keys, then values) are one flat run, of which a wave takes 256 (e4m3 128): four
 // loads in flight per lane (two) before the chain offsets -> length -> page -> store begins, which
 // one lane per token walks for the wave (up to nine tokens, their requests counted by ballots).
-// Measured from memory: 16,372 tokens into bf16 pages 33.4 us = 4.3 TB/s, 36,257 into e4m3 pages 61 us = 3.9 TB/s;
+// Measured from memory: 16,372 tokens into bf16 pages 33.3 us = 4.3 TB/s, 36,257 into e4m3 pages 61 us = 3.8 TB/s;
 // a large copy reaches 5.1.
 #include "kv.hpp"
 

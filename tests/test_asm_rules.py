@@ -100,11 +100,11 @@ def test_scalar_operands_of_memory_instructions_have_arrived():
 
 @needs_hipcc
 def test_no_store_into_lds_is_pending_at_a_barrier():
-    found = generated()["kv_attention_mfma.hip"]
-    main = {k: v for k, v in found.items() if "kv_attention_mfma" in k}
-    assert len(main) == 8 and len(found) > 8
-    for name, code in found.items():
-        assert not pending_stores(code), name
+    for source, found in generated().items():
+        for name, code in found.items():
+            assert not pending_stores(code), (source, name)
+    main = {k: v for k, v in generated()["kv_attention_mfma.hip"].items() if "kv_attention_mfma" in k}
+    assert len(main) == 8
     for name, code in main.items():
         assert sum(x.op.startswith("ds_write") for x in code) > 10 and sum(x.op == "s_barrier" for x in code) > 8
         bad = pending_stores(code, written_waits=True)
